@@ -324,14 +324,15 @@ def _gemm_own(s):
 
 
 def _adamw_own(s):
-    from block_scaled_fp4_hadamard_amd import AdamWState, adamw_step
-    t = s["tensors"]
-    if "states" not in s:        # the optimizer's state objects around the state tensors, kept as a user keeps them
-        s["states"] = [AdamWState(x["m"], x["v"], x.get("m_scale"), x.get("v_scale")) for x in t]
+    from block_scaled_fp4_hadamard_amd import AdamWState, AdamWTensors, adamw_step
+    if "list" not in s:          # a trainer makes the list of its weights, gradients and states once
+        t = s["tensors"]
+        s["list"] = AdamWTensors([x["w"] for x in t], [x["g"] for x in t],
+                                 [AdamWState(x["m"], x["v"], x.get("m_scale"), x.get("v_scale")) for x in t],
+                                 copies=[x["copy"] for x in t])
     s["step"] += 1
-    adamw_step([x["w"] for x in t], [x["g"] for x in t], s["states"], lr=LR, step=s["step"], beta1=BETA1, beta2=BETA2,
-               eps=EPS, weight_decay=DECAY, rounding=s["rounding"], seed=s["seed"] + s["step"],
-               copies=[x["copy"] for x in t])
+    adamw_step(s["list"], lr=LR, step=s["step"], beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY,
+               rounding=s["rounding"], seed=s["seed"] + s["step"])
 
 
 def run(state):

@@ -7,3 +7,5 @@ wrappers (torch supplies device memory and streams only), the training-step
 orchestration of the three GEMMs, and the seeded synthetic inputs.
 """
 from .api import QTensor, quantize, gemm, gemm_grouped, empty_qtensor, mxnorm_quantize  # noqa: F401
+from .api import Fp8Tensor, fp8_quantize, fp8_gemm, empty_fp8  # noqa: F401
+from .api import AdamWState, AdamWTensors, adamw_step  # noqa: F401

@@ -16,10 +16,12 @@ AXIS = {"row": 1, "col": 2, "both": 3}
 HAD = {"none": 0, "det": 1, "rand": 2}
 OUT = {"f32": 0, "bf16": 1}
 OSCI = {"init": 0, "track": 1, "check": 2}
+FP8_FMT = {"e4m3": 0, "e5m2": 1}
+FP8_KIND = {"line": 0, "tile": 1}
 
 EXPORTS = ("mx_quantize", "mx_hadamard_quantize", "mx_gemm", "mx_gemm_grouped", "mx_mxnorm_quantize", "mx_quant_stats",
-           "mx_nvfp4_quantize", "mx_hadamard_rotate", "mx_quantize_f32", "mx_osci_reset", "mx_status_str",
-           "mx_version")
+           "mx_nvfp4_quantize", "mx_hadamard_rotate", "mx_quantize_f32", "mx_osci_reset", "mx_fp8_quantize",
+           "mx_fp8_gemm", "mx_adamw_step", "mx_status_str", "mx_version")
 
 
 class MXError(RuntimeError):
@@ -37,6 +39,23 @@ class NVTensorC(ctypes.Structure):
 class QTensorC(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
                 ("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64)]
+
+
+class Fp8TensorC(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64)]
+
+
+class AdamwTensorC(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("grad", ctypes.c_int32)]
+
+
+class AdamwParamsC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("step_dev", ctypes.c_void_p), ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
 GEMM_GROUP_MAX = 8      # MX_GEMM_GROUP_MAX
@@ -80,6 +99,13 @@ def lib():
         L.mx_quantize_f32.restype = ctypes.c_int
         L.mx_osci_reset.argtypes = [vp, i64, i64, i64, qp, i32, vp, vp, vp, vp, i64, i32, ctypes.c_float, vp, vp]
         L.mx_osci_reset.restype = ctypes.c_int
+        fp = ctypes.POINTER(Fp8TensorC)
+        L.mx_fp8_quantize.argtypes = [vp, i64, i64, i64, i32, i32, i32, fp, fp, vp]
+        L.mx_fp8_quantize.restype = ctypes.c_int
+        L.mx_fp8_gemm.argtypes = [fp, i32, fp, i32, i32, i64, i64, i64, vp, i64, i32, vp]
+        L.mx_fp8_gemm.restype = ctypes.c_int
+        L.mx_adamw_step.argtypes = [ctypes.POINTER(AdamwTensorC), i32, i32, ctypes.POINTER(AdamwParamsC), i32, u64, vp]
+        L.mx_adamw_step.restype = ctypes.c_int
         L.mx_status_str.argtypes = [ctypes.c_int]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_version.argtypes = []
@@ -159,3 +185,23 @@ def mx_osci_reset(w_ptr, rows, cols, ld_w, q, grid, w_prev, q_prev, dist_m, dist
                   resets_ptr, stream):
     return lib().mx_osci_reset(w_ptr, rows, cols, ld_w, ctypes.byref(q), grid, w_prev, q_prev, dist_m, dist_q,
                                ld_state, mode, threshold, resets_ptr, stream)
+
+
+def fp8_tensor(codes_ptr, ld_codes, scales_ptr, ld_scales):
+    return Fp8TensorC(codes_ptr, ld_codes, scales_ptr, ld_scales)
+
+
+def mx_fp8_quantize(x_ptr, rows, cols, ld_x, fmt, kind, axis, row_q, col_q, stream):
+    return lib().mx_fp8_quantize(x_ptr, rows, cols, ld_x, fmt, kind, axis,
+                                 ctypes.byref(row_q) if row_q is not None else None,
+                                 ctypes.byref(col_q) if col_q is not None else None, stream)
+
+
+def mx_fp8_gemm(a_q, a_fmt, b_q, b_fmt, b_kind, M, N, K, c_ptr, ldc, out, stream):
+    return lib().mx_fp8_gemm(ctypes.byref(a_q), a_fmt, ctypes.byref(b_q), b_fmt, b_kind, M, N, K, c_ptr, ldc, out,
+                             stream)
+
+
+def mx_adamw_step(tensors, count, bits, params, rnd, seed, stream):
+    """tensors: an array of AdamwTensorC; params: an AdamwParamsC."""
+    return lib().mx_adamw_step(tensors, count, bits, ctypes.byref(params), rnd, seed, stream)

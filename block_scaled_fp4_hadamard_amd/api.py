@@ -2,6 +2,7 @@
 the tensor's device and launch on torch's current stream.  No arithmetic of
 the method happens here.
 """
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -307,3 +308,265 @@ def nvfp4_quantize(x, axis="row", rounding="rtne", seed=0, row_out=None, col_out
                                 seed, rq, cq, _stream(dev))
     _lib.check(st, "mx_nvfp4_quantize")
     return out
+
+
+FP8_BLOCK = 128           # values per scale (MX_FP8_BLOCK)
+
+
+def _fp8_blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def _pitch(t, name):
+    """Elements between the rows of a 2-D tensor with unit column stride whose rows do not overlap."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("%s: its rows overlap (a stride of %d for %d columns)" % (name, t.stride(0), t.shape[1]))
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _launch_on(dev):
+    """Refuses host tensors, and makes dev the current device for a launch on its stream."""
+    if dev.type != "cuda":
+        raise ValueError("the operands must be CUDA tensors, got %s" % dev)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+@dataclass
+class Fp8Tensor:
+    """A block-scaled 8-bit operand: L lines of length k, K-contiguous.
+
+    codes  uint8 (L, 128 * ceil(k / 128)): E4M3 or E5M2 bytes, zeros past k
+    scales float32: kind "line" (ceil(k / 128), L), one per line and 128 values; kind "tile"
+           (ceil(L / 128), ceil(k / 128)), one per 128 lines x 128 values
+    """
+    codes: torch.Tensor
+    scales: torch.Tensor
+    k: int
+    fmt: str = "e4m3"
+    kind: str = "line"
+
+    @property
+    def lines(self):
+        return self.codes.shape[0]
+
+    def check(self, name):
+        if self.fmt not in _lib.FP8_FMT or self.kind not in _lib.FP8_KIND:
+            raise ValueError("%s: unknown format %r or kind %r" % (name, self.fmt, self.kind))
+        kb = _fp8_blocks(self.k)
+        if self.codes.dtype != torch.uint8 or self.codes.dim() != 2 or self.codes.shape[1] != kb * FP8_BLOCK:
+            raise ValueError("%s: codes must be uint8 (lines, %d) for k = %d" % (name, kb * FP8_BLOCK, self.k))
+        lines = self.codes.shape[0]
+        shape = (kb, lines) if self.kind == "line" else (_fp8_blocks(lines), kb)
+        if self.scales.dtype != torch.float32 or tuple(self.scales.shape) != shape:
+            raise ValueError("%s: scales must be float32 %s for kind %r" % (name, shape, self.kind))
+        _pitch(self.codes, name + ".codes")
+        _pitch(self.scales, name + ".scales")
+        if self.scales.device != self.codes.device:
+            raise ValueError("%s: codes and scales are on different devices" % name)
+
+    def c_struct(self):
+        return _lib.fp8_tensor(self.codes.data_ptr(), _pitch(self.codes, "codes"),
+                               self.scales.data_ptr(), _pitch(self.scales, "scales"))
+
+
+def empty_fp8(lines, k, device, fmt="e4m3", kind="line"):
+    """An uninitialised output operand."""
+    kb = _fp8_blocks(k)
+    shape = (kb, lines) if kind == "line" else (_fp8_blocks(lines), kb)
+    return Fp8Tensor(torch.empty((lines, kb * FP8_BLOCK), dtype=torch.uint8, device=device),
+                     torch.empty(shape, dtype=torch.float32, device=device), k, fmt, kind)
+
+
+def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=None):
+    """Cast a 2-D bf16 CUDA tensor to 8 bits with a float32 scale for each block of 128 (a line's 128 values, kind
+    "line", or a 128 x 128 tile, "tile"); {"row": Fp8Tensor of x's rows, "col": of its columns} as requested.
+
+    x needs a column count and a row stride that are multiples of 8.
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    if axis not in _lib.AXIS or kind not in _lib.FP8_KIND or fmt not in _lib.FP8_FMT:
+        raise ValueError("unknown axis %r, kind %r or format %r" % (axis, kind, fmt))
+    xb = _bits_view(x)
+    rows, cols = x.shape
+    dev = x.device
+    out = {}
+    rq = cq = None
+    for name, given, lines, k in (("row", row_out, rows, cols), ("col", col_out, cols, rows)):
+        if axis not in (name, "both"):
+            continue
+        q = given
+        if q is None:
+            q = empty_fp8(lines, k, dev, fmt, kind)
+        else:
+            q.check(name + "_out")
+            if (q.lines, q.k, q.fmt, q.kind) != (lines, k, fmt, kind) or q.codes.device != dev:
+                raise ValueError("%s_out is not an %s operand of %d %s lines of %d values on %s"
+                                 % (name, fmt, lines, kind, k, dev))
+        out[name] = q
+        if name == "row":
+            rq = q.c_struct()
+        else:
+            cq = q.c_struct()
+    with _launch_on(dev):
+        st = _lib.mx_fp8_quantize(xb.data_ptr(), rows, cols, _pitch(x, "x"),
+                                  _lib.FP8_FMT[fmt], _lib.FP8_KIND[kind], _lib.AXIS[axis], rq, cq, _stream(dev))
+    _lib.check(st, "mx_fp8_quantize")
+    return out
+
+
+def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
+    """C = A B^T (M x N) on two 8-bit operands' values, fp32 accumulation, fp32 or bf16 output.
+
+    a is scaled by lines (kind "line"), b by lines or tiles; each may be E4M3 or E5M2.
+    """
+    a.check("a")
+    b.check("b")
+    if a.k != b.k:
+        raise ValueError("operands disagree on K: %d vs %d" % (a.k, b.k))
+    if a.kind != "line":
+        raise ValueError("a must be scaled by lines, got kind %r" % a.kind)
+    dev = a.codes.device
+    M, N = a.lines, b.lines
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    elif out.dim() != 2 or out.shape[0] != M or out.shape[1] != N:
+        raise ValueError("out must be a row-major (%d, %d) view" % (M, N))
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the output must be float32 or bfloat16, got %s" % out.dtype)
+    if b.codes.device != dev or out.device != dev:
+        raise ValueError("a, b and out must be on one device")
+    kind = "f32" if out.dtype == torch.float32 else "bf16"
+    with _launch_on(dev):
+        st = _lib.mx_fp8_gemm(a.c_struct(), _lib.FP8_FMT[a.fmt], b.c_struct(), _lib.FP8_FMT[b.fmt],
+                              _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), _pitch(out, "out"),
+                              _lib.OUT[kind], _stream(dev))
+    _lib.check(st, "mx_fp8_gemm")
+    return out
+
+
+@dataclass
+class AdamWState:
+    """AdamW's moments of one tensor of n elements: float32 m and v, or (8 bits) uint8 E4M3 m and E5M3 v with float32
+    scales for each 128 elements."""
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: torch.Tensor = None
+    v_scale: torch.Tensor = None
+
+    @staticmethod
+    def zeros_like(w, bits=32):
+        """The state of a first step: all moments zero."""
+        if bits == 32:
+            return AdamWState(torch.zeros_like(w), torch.zeros_like(w))
+        if bits != 8:
+            raise ValueError("states are held in 8 or 32 bits, not %r" % (bits,))
+        codes = [torch.zeros(w.shape, dtype=torch.uint8, device=w.device) for _ in range(2)]
+        scales = [torch.zeros(_fp8_blocks(w.numel()), dtype=torch.float32, device=w.device) for _ in range(2)]
+        return AdamWState(*codes, *scales)
+
+    @property
+    def bits(self):
+        return 8 if self.m.dtype == torch.uint8 else 32
+
+
+class AdamWTensors:
+    """The tensors that adamw_step updates, checked and laid out once: float32 master weights, their gradients
+    (float32 or bf16), their states (all of 8 or all of 32 bits) and, if given, the bf16 copies that a step writes.
+
+    Every tensor is contiguous, and none may be given twice.  The object holds the tensors themselves; one whose
+    storage is replaced (Tensor.data, resize_) needs a new object, and new gradient tensors go in by set_grads.
+    """
+
+    def __init__(self, params, grads, states, copies=None):
+        self.params, self.states = list(params), list(states)
+        self.copies = list(copies) if copies is not None else [None] * len(self.params)
+        if not len(self.params) == len(self.states) == len(self.copies):
+            raise ValueError("params, states and copies must have the same length")
+        self.device = self.params[0].device if self.params else None
+        self.bits = self.states[0].bits if self.states else 32
+        self._c = (_lib.AdamwTensorC * max(1, len(self.params)))()
+        starts = set()
+        for i, (w, s, h) in enumerate(zip(self.params, self.states, self.copies)):
+            self._hold(i, "weight", w, torch.float32, w.numel())
+            if s.bits != self.bits:
+                raise ValueError("tensor %d: every state must have %d bits" % (i, self.bits))
+            blocks = _fp8_blocks(w.numel())
+            state = torch.float32 if self.bits == 32 else torch.uint8
+            each = [("m", s.m, state, w.numel()), ("v", s.v, state, w.numel())]
+            if self.bits == 8:
+                each += [("m_scale", s.m_scale, torch.float32, blocks), ("v_scale", s.v_scale, torch.float32, blocks)]
+            if h is not None:
+                each.append(("copy", h, torch.bfloat16, w.numel()))
+            for name, x, dtype, n in each:
+                self._hold(i, name, x, dtype, n)
+            if w.numel():
+                mine = [w.data_ptr()] + [x.data_ptr() for _, x, _, _ in each]
+                if len(set(mine)) < len(mine) or not starts.isdisjoint(mine):
+                    raise ValueError("tensor %d: a weight, state or copy is given twice" % i)
+                starts.update(mine)
+            c = self._c[i]
+            c.w, c.m, c.v, c.n = w.data_ptr(), s.m.data_ptr(), s.v.data_ptr(), w.numel()
+            if self.bits == 8:
+                c.m_scales, c.v_scales = s.m_scale.data_ptr(), s.v_scale.data_ptr()
+            c.copy = h.data_ptr() if h is not None else None
+        self.set_grads(grads)
+
+    def _hold(self, i, name, x, dtype, n):
+        if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.numel() != n or not x.is_contiguous():
+            raise ValueError("tensor %d: its %s must be a contiguous %s tensor of %d elements" % (i, name, dtype, n))
+        if x.device != self.device:
+            raise ValueError("tensor %d: its %s is on %s, the first weight on %s" % (i, name, x.device, self.device))
+
+    def set_grads(self, grads):
+        """Other gradient tensors for the steps to come."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("%d gradients for %d weights" % (len(grads), len(self.params)))
+        for i, (g, w) in enumerate(zip(grads, self.params)):
+            if not isinstance(g, torch.Tensor) or g.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError("tensor %d: its gradient must be float32 or bfloat16" % i)
+            self._hold(i, "gradient", g, g.dtype, w.numel())
+        for i, g in enumerate(grads):
+            self._c[i].g = g.data_ptr()
+            self._c[i].grad = _lib.OUT["f32" if g.dtype == torch.float32 else "bf16"]
+        self.grads = grads
+
+
+def _scalar(value, dtype, name, dev):
+    """(host value, device address) of a number or of a one-element tensor."""
+    if not isinstance(value, torch.Tensor):
+        return value, None
+    if value.dtype != dtype or value.numel() != 1 or value.device != dev:
+        raise ValueError("%s must be a number or a one-element %s tensor on %s" % (name, dtype, dev))
+    return 0, value.data_ptr()
+
+
+def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, rounding="rtne", seed=0,
+               grad_scale=None):
+    """One AdamW step (decoupled weight decay) in place on an AdamWTensors: its weights, states and copies.
+
+    step counts from 1.  lr and step are numbers, or one-element CUDA tensors (float32, int64) that the kernel reads,
+    so that a captured graph replays with values that move on.  rounding and seed are those of 8-bit states: "rtne", or
+    "sr" with another seed for each step.  grad_scale: a one-element float32 CUDA tensor that every gradient is
+    multiplied by first (clipping, loss scaling).
+    """
+    if rounding not in _lib.ROUND:
+        raise ValueError("unknown rounding %r" % (rounding,))
+    dev = tensors.device
+    lr, lr_dev = _scalar(lr, torch.float32, "lr", dev)
+    step, step_dev = _scalar(step, torch.int64, "step", dev)
+    scale = None
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor):
+            raise ValueError("grad_scale must be a one-element torch.float32 tensor on %s" % dev)
+        _, scale = _scalar(grad_scale, torch.float32, "grad_scale", dev)
+    params = _lib.AdamwParamsC(lr, beta1, beta2, eps, weight_decay, step, step_dev, lr_dev, scale)
+    with _launch_on(dev) if dev is not None else contextlib.nullcontext():
+        st = _lib.mx_adamw_step(tensors._c, len(tensors.params), tensors.bits, params, _lib.ROUND[rounding], seed,
+                                _stream(dev) if dev is not None else None)
+    _lib.check(st, "mx_adamw_step")

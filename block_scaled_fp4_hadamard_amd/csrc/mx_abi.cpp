@@ -4,7 +4,9 @@
 // device.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <math.h>
 #include "mx_kernels.h"
+#include "fp8_kernels.h"
 
 namespace {
 
@@ -146,6 +148,25 @@ mx_status gemm_args(const mx_qtensor* a, const mx_qtensor* b, int64_t M, int64_t
   p.c = c;
   p.ldc = ldc;
   return MX_OK;
+}
+
+int64_t fp8_blocks(int64_t n) { return n / mx::kFp8Block + (n % mx::kFp8Block != 0); }
+
+bool fp8_fmt_ok(int fmt) { return fmt == MX_FP8_E4M3 || fmt == MX_FP8_E5M2; }
+bool fp8_kind_ok(int kind) { return kind == MX_FP8_LINE || kind == MX_FP8_TILE; }
+
+mx_status check_fp8(const mx_fp8_tensor* q, int64_t lines, int64_t k, int kind) {
+  if (q == nullptr || q->codes == nullptr || q->scales == nullptr) return MX_ERR_INVALID;
+  if (!aligned16(q->codes) || ((uintptr_t)q->scales & 3u) != 0) return MX_ERR_INVALID;
+  if (q->ld_codes % 16 != 0 || q->ld_codes / mx::kFp8Block < fp8_blocks(k)) return MX_ERR_INVALID;
+  if (q->ld_scales < (kind == MX_FP8_LINE ? lines : fp8_blocks(k))) return MX_ERR_INVALID;
+  return MX_OK;
+}
+
+// more 128 x 128 tiles than one launch's grid can number
+bool too_many_tiles(int64_t m, int64_t n) {
+  return fp8_blocks(m) >= (int64_t(1) << 31) || fp8_blocks(n) >= (int64_t(1) << 31) ||
+         fp8_blocks(m) * fp8_blocks(n) >= (int64_t(1) << 31);
 }
 
 }  // namespace
@@ -397,6 +418,128 @@ mx_status mx_osci_reset(float* w, int64_t rows, int64_t cols, int64_t ld_w, cons
   p.resets = (unsigned long long*)resets;
   hipError_t e = mx::launch_osci(p, grid, (hipStream_t)hip_stream);
   return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+mx_status mx_fp8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, mx_fp8_fmt fmt,
+                          mx_fp8_kind kind, mx_axis axis, const mx_fp8_tensor* row_out, const mx_fp8_tensor* col_out,
+                          void* hip_stream) {
+  if (rows < 0 || cols < 0) return MX_ERR_INVALID;
+  if (!fp8_fmt_ok(fmt) || !fp8_kind_ok(kind)) return MX_ERR_INVALID;
+  if (axis != MX_AXIS_ROW && axis != MX_AXIS_COL && axis != MX_AXIS_BOTH) return MX_ERR_INVALID;
+  if (rows == 0 || cols == 0) return MX_OK;
+  if (x == nullptr || !aligned16(x)) return MX_ERR_INVALID;
+  if (ld_x < cols || ld_x % 8 != 0 || cols % 8 != 0 || too_many_tiles(rows, cols)) return MX_ERR_INVALID;
+  const bool do_row = (axis & MX_AXIS_ROW) != 0, do_col = (axis & MX_AXIS_COL) != 0;
+  if (do_row) {
+    const mx_status s = check_fp8(row_out, rows, cols, kind);
+    if (s != MX_OK) return s;
+  }
+  if (do_col) {
+    const mx_status s = check_fp8(col_out, cols, rows, kind);
+    if (s != MX_OK) return s;
+  }
+  mx::Fp8QuantParams p{};
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.ld_x = ld_x;
+  if (do_row) {
+    p.row_codes = row_out->codes;
+    p.ld_row_codes = row_out->ld_codes;
+    p.row_scales = row_out->scales;
+    p.ld_row_scales = row_out->ld_scales;
+  }
+  if (do_col) {
+    p.col_codes = col_out->codes;
+    p.ld_col_codes = col_out->ld_codes;
+    p.col_scales = col_out->scales;
+    p.ld_col_scales = col_out->ld_scales;
+  }
+  const hipError_t e = mx::launch_fp8_quant(p, fmt, kind, do_row, do_col, (hipStream_t)hip_stream);
+  return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_tensor* b, mx_fp8_fmt b_fmt,
+                      mx_fp8_kind b_kind, int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, mx_out out,
+                      void* hip_stream) {
+  if (M < 0 || N < 0 || K <= 0) return MX_ERR_INVALID;
+  if (!fp8_fmt_ok(a_fmt) || !fp8_fmt_ok(b_fmt) || !fp8_kind_ok(b_kind)) return MX_ERR_INVALID;
+  if (out != MX_OUT_F32 && out != MX_OUT_BF16) return MX_ERR_INVALID;
+  if (M == 0 || N == 0) return MX_OK;
+  mx_status s = check_fp8(a, M, K, MX_FP8_LINE);
+  if (s != MX_OK) return s;
+  s = check_fp8(b, N, K, b_kind);
+  if (s != MX_OK) return s;
+  const uintptr_t esize = out == MX_OUT_F32 ? 4u : 2u;
+  if (c == nullptr || ((uintptr_t)c % esize) != 0 || ldc < N || too_many_tiles(M, N)) return MX_ERR_INVALID;
+  mx::Fp8GemmParams p{};
+  p.a_codes = a->codes;
+  p.b_codes = b->codes;
+  p.a_scales = a->scales;
+  p.b_scales = b->scales;
+  p.lda = a->ld_codes;
+  p.ldb = b->ld_codes;
+  p.lda_scales = a->ld_scales;
+  p.ldb_scales = b->ld_scales;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.c = c;
+  p.ldc = ldc;
+  const hipError_t e = mx::launch_fp8_gemm(p, a_fmt, b_fmt, b_kind, out, (hipStream_t)hip_stream);
+  return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t bits, const mx_adamw_params* params,
+                        mx_round round, uint64_t seed, void* hip_stream) {
+  if (count < 0 || (count > 0 && tensors == nullptr) || params == nullptr) return MX_ERR_INVALID;
+  if (bits != 8 && bits != 32) return MX_ERR_INVALID;
+  if (round != MX_ROUND_RTNE && round != MX_ROUND_SR) return MX_ERR_INVALID;
+  if (bits == 32 && round != MX_ROUND_RTNE) return MX_ERR_INVALID;
+  const mx_adamw_params& q = *params;
+  if (!(q.beta1 >= 0.0 && q.beta1 < 1.0) || !(q.beta2 >= 0.0 && q.beta2 < 1.0)) return MX_ERR_INVALID;
+  if (!(q.eps >= 0.0) || !isfinite(q.eps) || !isfinite(q.weight_decay)) return MX_ERR_INVALID;
+  if (q.lr_dev == nullptr ? !isfinite(q.lr) : ((uintptr_t)q.lr_dev & 3u) != 0) return MX_ERR_INVALID;
+  if (q.step_dev == nullptr ? q.step < 1 : ((uintptr_t)q.step_dev & 7u) != 0) return MX_ERR_INVALID;
+  if (((uintptr_t)q.grad_scale & 3u) != 0) return MX_ERR_INVALID;
+  const uintptr_t state = bits == 32 ? 3u : 0u;
+  for (int32_t i = 0; i < count; ++i) {
+    const mx_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n >= (int64_t(1) << 40)) return MX_ERR_INVALID;
+    if (t.grad != MX_OUT_F32 && t.grad != MX_OUT_BF16) return MX_ERR_INVALID;
+    if (t.n == 0) continue;
+    if (t.w == nullptr || t.g == nullptr || t.m == nullptr || t.v == nullptr) return MX_ERR_INVALID;
+    if (((uintptr_t)t.w & 3u) || ((uintptr_t)t.g & (t.grad == MX_OUT_F32 ? 3u : 1u))) return MX_ERR_INVALID;
+    if (((uintptr_t)t.m & state) || ((uintptr_t)t.v & state) || ((uintptr_t)t.copy & 1u)) return MX_ERR_INVALID;
+    if (bits == 8) {
+      if (t.m_scales == nullptr || t.v_scales == nullptr) return MX_ERR_INVALID;
+      if (((uintptr_t)t.m_scales & 3u) || ((uintptr_t)t.v_scales & 3u)) return MX_ERR_INVALID;
+    }
+  }
+  mx::AdamwStep step{};
+  step.lr = q.lr;
+  step.beta1 = q.beta1;
+  step.beta2 = q.beta2;
+  step.eps = q.eps;
+  step.weight_decay = q.weight_decay;
+  step.step = q.step;
+  step.step_dev = q.step_dev;
+  step.lr_dev = q.lr_dev;
+  step.grad_scale = q.grad_scale;
+  step.seed = seed;
+  for (int32_t at = 0; at < count; at += mx::kAdamwGroup) {
+    mx::AdamwTensor group[mx::kAdamwGroup];
+    bool bf16[mx::kAdamwGroup];
+    const int n = count - at < mx::kAdamwGroup ? count - at : mx::kAdamwGroup;
+    for (int i = 0; i < n; ++i) {
+      const mx_adamw_tensor& t = tensors[at + i];
+      group[i] = mx::AdamwTensor{t.w, t.g, t.m, t.v, t.m_scales, t.v_scales, t.copy, t.n};
+      bf16[i] = t.grad == MX_OUT_BF16;
+    }
+    const hipError_t e = mx::launch_adamw(group, bf16, n, at, step, bits, round, (hipStream_t)hip_stream);
+    if (e != hipSuccess) return MX_ERR_DEVICE;
+  }
+  return MX_OK;
 }
 
 const char* mx_status_str(mx_status status) {

@@ -350,6 +350,132 @@ mx_status mx_osci_reset(float *w, int64_t rows, int64_t cols, int64_t ld_w, cons
                         float *w_prev, float *q_prev, float *dist_m, float *dist_q, int64_t ld_state,
                         mx_osci_mode mode, float threshold, uint64_t *resets, void *hip_stream);
 
+/*
+ * 8-bit floating-point operands with a float32 scale for each block of 128
+ * values.  The MXFP4 recipe is enabled one GEMM at a time, the others staying
+ * in 8 bits ("Pre-addestramento ... con MXFP4", Metodologia: Fprop, then
+ * Dgrad, then Wgrad on FP4 against an FP8 baseline); these are the operands
+ * and the product of the GEMMs that stay.
+ *
+ * An operand (mx_fp8_tensor) holds L lines of length K, K-contiguous:
+ *   codes   [L][128 * ceil(K / 128)] bytes, E4M3 (finite, largest 448) or E5M2
+ *           (largest finite 57344); the bytes past K are zero: the quantizer
+ *           writes them, and the product counts on them
+ *   scales  MX_FP8_LINE: one per line and 128 values, block-major:
+ *           scale of line l, block b at scales[b * ld_scales + l];
+ *           MX_FP8_TILE: one per 128 lines x 128 values, at
+ *           scales[(l / 128) * ld_scales + b]
+ * A value is code * scale.
+ */
+#define MX_FP8_BLOCK 128
+typedef enum { MX_FP8_E4M3 = 0, MX_FP8_E5M2 = 1 } mx_fp8_fmt;
+typedef enum { MX_FP8_LINE = 0, MX_FP8_TILE = 1 } mx_fp8_kind;
+
+typedef struct {
+  uint8_t *codes;     /* device, 16-byte aligned */
+  int64_t ld_codes;   /* bytes between lines; >= 128 * ceil(K / 128), multiple of 16 */
+  float *scales;      /* device, 4-byte aligned */
+  int64_t ld_scales;  /* floats; >= L (MX_FP8_LINE) or ceil(K / 128) (MX_FP8_TILE) */
+} mx_fp8_tensor;
+
+/*
+ * mx_fp8_quantize: the 8-bit cast of a bf16 matrix.  Per block (a line's 128
+ * values, or a 128 x 128 tile; the last ones of an axis may be part-filled):
+ *   s = max(RN32(amax / F), 2^-126), F = 448 or 57344;  r = RN32(1 / s);
+ *   code = RN32(x * r) rounded to nearest even in the format.
+ * A block holding Inf or NaN gets s = NaN and codes 0.
+ *   x, rows, cols, ld_x  device, 16-byte aligned bf16 bit patterns; any rows,
+ *              cols % 8 == 0, ld_x >= cols and a multiple of 8; either size
+ *              0: nothing to do, MX_OK
+ *   fmt, kind  of every output
+ *   axis       which outputs: row_out holds rows lines of length cols, col_out
+ *              the transpose, cols lines of length rows; both come from one
+ *              read of x, and MX_FP8_TILE gives both the same scales
+ */
+mx_status mx_fp8_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x, mx_fp8_fmt fmt,
+                          mx_fp8_kind kind, mx_axis axis, const mx_fp8_tensor *row_out,
+                          const mx_fp8_tensor *col_out, void *hip_stream);
+
+/*
+ * mx_fp8_gemm: C[m][n] = sum_k A[m][k] * B[n][k] on the operands' values:
+ * each block of 128 k summed on the matrix cores, its two scales multiplied in
+ * float32 (a product of scales that overflows float32 gives Inf or NaN), the
+ * blocks added in float32 in order.  For fp32 output a block's products are
+ * exact and its sum is float32, |err| <= (128 * 2^-23 + (K / 128 + 2) * 2^-24)
+ * * sum |a b|.  For bf16 output the 8-bit matrix instruction sums them, twice as
+ * fast: among each 8 neighbouring k it drops what lies below 2^-13 of the
+ * largest product, |err| < 2^-10 * sum |a b| before the rounding to bf16 (about
+ * 1.5e-5 of the result's norm on normal data).
+ *   a          M lines of length K, scales MX_FP8_LINE
+ *   b          N lines of length K, scales of b_kind
+ *   M, N, K    any; M or N 0: nothing to do, K <= 0 is rejected
+ *   c, ldc     device, row-major [M][ldc], fp32 or bf16 (round to nearest even
+ *              of the fp32 result), aligned to its element size, ldc >= N;
+ *              must not overlap an operand
+ * Rows of C that start 16-byte aligned (c and ldc) are written fastest.
+ */
+mx_status mx_fp8_gemm(const mx_fp8_tensor *a, mx_fp8_fmt a_fmt, const mx_fp8_tensor *b, mx_fp8_fmt b_fmt,
+                      mx_fp8_kind b_kind, int64_t M, int64_t N, int64_t K, void *c, int64_t ldc, mx_out out,
+                      void *hip_stream);
+
+/*
+ * mx_adamw_step: one AdamW step (decoupled weight decay) over a list of
+ * float32 master weights, the weights that mx_quantize_f32 casts and
+ * mx_osci_reset tracks.  Per element, in float32 with one rounding per
+ * operation, in this order (t = step; the coefficients in parentheses are
+ * formed in float64 and rounded to float32 once):
+ *   g = g * grad_scale                           (if one is given)
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + g * (1 - beta2) * g
+ *   d = sqrt(v) * (1 / sqrt(1 - beta2^t)) + eps
+ *   w = w * (1 - lr * weight_decay) - m / d * (lr / (1 - beta1^t))
+ *   copy = w as bf16, to nearest even            (if one is given)
+ * bits 32: m and v are float32.  bits 8: they are held in 8 bits with a
+ * float32 scale for each 128 elements (counted from the tensor's first; the
+ * last block may be part-filled), decoded as code * scale before the step and
+ * cast after it:
+ *   m  E4M3, F = 448;  v  E5M3 (unsigned: 5 exponent and 3 mantissa bits, a
+ *   float16's bits 14..7, codes to 0xF7), F = 61440;
+ *   s = max(RN32(amax / F), 2^-126), y = RN32(value * RN32(1 / s)) rounded by
+ *   MX_ROUND_RTNE or stochastically as mx_quantize rounds (16-bit draws;
+ *   element i of tensor k takes stream 4 + 2k for m, 5 + 2k for v, key seed);
+ *   a v above 0 keeps at least code 1; a block of m or v holding Inf or NaN
+ *   gets s = NaN and codes 0.
+ * w and copy come from the moments before that cast.
+ *   tensors    host array of count entries, read before the call returns; any
+ *              count (one launch for each 48); n = 0 entries are skipped; the
+ *              arrays of all entries must not overlap, and each is aligned to
+ *              its element (w, m, v, g, copy 16-byte aligned, 8-bit m and v
+ *              8-byte aligned: fastest)
+ *   step       t >= 1; if step_dev is not NULL the device's int64 is read
+ *              instead when the kernel runs (it must be >= 1), so that a
+ *              captured graph can be replayed with a step that moves on
+ *   lr         likewise, or the float32 at lr_dev
+ *   grad_scale NULL, or a device float32 (the clipping or loss-scale factor)
+ *   round      MX_ROUND_RTNE; MX_ROUND_SR with bits 8 only
+ *   seed       keys the draws; pass another one each step
+ */
+typedef struct {
+  float *w;
+  const void *g;        /* float32 or bf16, by grad */
+  void *m, *v;          /* float32, or codes (bits 8) */
+  float *m_scales, *v_scales;   /* [ceil(n / 128)], bits 8 only */
+  uint16_t *copy;       /* bf16 bit patterns, or NULL */
+  int64_t n;
+  mx_out grad;          /* MX_OUT_F32 or MX_OUT_BF16 */
+} mx_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const int64_t *step_dev;
+  const float *lr_dev;
+  const float *grad_scale;
+} mx_adamw_params;
+
+mx_status mx_adamw_step(const mx_adamw_tensor *tensors, int32_t count, int32_t bits,
+                        const mx_adamw_params *params, mx_round round, uint64_t seed, void *hip_stream);
+
 /* A static, human-readable name for a status code. */
 const char *mx_status_str(mx_status status);
 

@@ -11,7 +11,7 @@
 //
 // 8-bit moments: m is E4M3, v (never negative) E5M3, that is a float16 without
 // its sign and its last 7 mantissa bits, top code 0xF7 (61440).  A block's
-// scale is s = max(RN(amax / F), 2^-126), F = 448 or 61440, and a code rounds
+// scale is s = max(RN(amax * RN(1 / F)), 2^-126), F = 448 or 61440, and a code rounds
 // y = RN(value * RN(1 / s)) by RTNE or stochastically; a v above 0 never
 // rounds to code 0, so that a weight whose m is not 0 never meets d = eps.
 // The exponent range is why v has a format of its own: a block's v spans twice
@@ -107,13 +107,14 @@ __device__ __forceinline__ uint32_t code3(float y, uint32_t u) {
 
 // The eight codes of a lane's part of a block and the block's scale.
 template <bool FIRST, int ROUND>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint64_t group, uint32_t stream, uint64_t seed, float& s) {
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint64_t group, uint32_t stream, uint64_t seed,
+                                         float& s) {
   uint32_t top = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   top = row_max(top);
   const bool bad = top >= 0x7F800000u;
-  s = fmaxf(__uint_as_float(top) / (FIRST ? 448.0f : 61440.0f), 0x1p-126f);
+  s = fmaxf(__uint_as_float(top) * (FIRST ? 1.0f / 448.0f : 1.0f / 61440.0f), 0x1p-126f);
   const float r = 1.0f / s;
   if (bad) s = __uint_as_float(0x7FC00000u);
   uint32_t u[8] = {};

@@ -124,19 +124,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
 }
 
+// 16 bytes at any address that a row of C may start at: one store, whatever the row pitch
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef v4f v4f_any __attribute__((aligned(4)));
+
 // Sixteen consecutive columns of one row of C from a lane's accumulators.
 template <int OUT>
-__device__ __forceinline__ void store16(const Fp8GemmParams& p, int64_t m, int64_t n, const v4f (&acc)[4], bool wide) {
+__device__ __forceinline__ void store16(const Fp8GemmParams& p, int64_t m, int64_t n, const v4f (&acc)[4]) {
   if (m >= p.M || n >= p.N) return;
   const int64_t at = m * p.ldc + n;
-  if (wide && n + 16 <= p.N) {
+  if (n + 16 <= p.N) {
     if constexpr (OUT == MX_OUT_F32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *(v4f*)((float*)p.c + at + 4 * j) = acc[j];
+      for (int j = 0; j < 4; ++j) *(v4f_any*)((float*)p.c + at + 4 * j) = acc[j];
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *(u32x4*)((uint16_t*)p.c + at + 8 * h) =
+        *(u32x4_any*)((uint16_t*)p.c + at + 8 * h) =
             u32x4{pack_bf16(acc[2 * h][0], acc[2 * h][1]), pack_bf16(acc[2 * h][2], acc[2 * h][3]),
                   pack_bf16(acc[2 * h + 1][0], acc[2 * h + 1][1]), pack_bf16(acc[2 * h + 1][2], acc[2 * h + 1][3])};
     }
@@ -158,7 +162,7 @@ __device__ __forceinline__ void store16(const Fp8GemmParams& p, int64_t m, int64
 constexpr int kGT = 128, kGThreads = 256;
 
 template <int AF, int BF, int KIND, int OUT>
-__global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, int64_t tiles_m, bool wide) {
+__global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, int64_t tiles_m) {
   __shared__ __attribute__((aligned(16))) uint8_t sA[kGT * kKB], sB[kGT * kKB];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t m0 = (blockIdx.x % tiles_m) * kGT, n0 = (blockIdx.x / tiles_m) * kGT;
@@ -220,19 +224,244 @@ __global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, i
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) store16<OUT>(p, m0 + wm + 16 * i + lrow, col, acc[i], wide);
+  for (int i = 0; i < 4; ++i) store16<OUT>(p, m0 + wm + 16 * i + lrow, col, acc[i]);
 }
 
-// rows of C start 16-byte aligned and are a whole number of 16-byte pieces apart
-bool wide_rows(const Fp8GemmParams& p, int out_kind) {
-  return (uintptr_t)p.c % 16 == 0 && p.ldc % (out_kind == MX_OUT_F32 ? 4 : 8) == 0;
+// ---------------------------------------------------------------------------
+// Large products: a persistent grid, one workgroup per CU, each walking 256 x
+// 256 tiles of C with eight waves of 128 x 64 (two waves per SIMD).  K advances
+// one block (a 128-byte line of every operand row) per step, copied global ->
+// LDS by DMA into one of two 64 KB stages while the other is consumed.
+//
+// A wave holds the step's four B fragments and streams its eight A fragments;
+// row i's four matrix instructions run beside the fused multiply-adds of row
+// i - 1, so their results are never waited for.  The step's last two rows run
+// column by column after the barrier that frees the stage: a B fragment is
+// replaced by the next step's as soon as its two instructions are issued, which
+// hides the next step's first LDS reads behind the last quarter of this one.
+//
+// Rows of a tile past the operand's last line read that line again (their
+// results are not stored), so every copy stays inside the operand and any M
+// and N run here.
+constexpr int kBT = 256, kBThreads = 512, kXcds = 8, kGroupM = 4, kGroupN = 8;
+constexpr int kStage = kBT * kKB;
+
+// Global -> LDS copy of 16 (4) bytes per lane: LDS address = M0 + size * lane.  Inline asm, so that the
+// compiler places no waits of its own for it; it writes no register.  An SALU write of M0 needs one wait
+// state before the copy reads it.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const T*)(((uint64_t)hi << 32) | lo);
+}
+
+// Tiles are dealt in groups of 4 (M) x 8 (N) to the 8 XCDs, a group to the 32 CUs of one, so that the tiles
+// an XCD computes at once share 4 A strips and 8 B strips in its L2.
+struct BigMap {
+  int tiles_m, tiles_n, groups_m, groups, rounds;
+};
+
+__device__ __forceinline__ int next_tile(const BigMap& t, int r, int& bm, int& bn) {
+  const int xcd = blockIdx.x % kXcds, member = blockIdx.x / kXcds;
+  for (; r < t.rounds; ++r) {
+    const int g = r * kXcds + xcd;
+    if (g >= t.groups) return t.rounds;
+    bm = (g % t.groups_m) * kGroupM + member % kGroupM;
+    bn = (g / t.groups_m) * kGroupN + member / kGroupM;
+    if (bm < t.tiles_m && bn < t.tiles_n) return r;
+  }
+  return t.rounds;
+}
+
+template <int AF, int BF, int KIND>
+__global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p, const BigMap map) {
+  __shared__ __attribute__((aligned(1024))) uint8_t sA[2][kStage], sB[2][kStage];
+  __shared__ __attribute__((aligned(1024))) float sSA[2][kBT], sSB[2][kBT];
+
+  int bm = 0, bn = 0;
+  int r = next_tile(map, 0, bm, bn);
+  if (r >= map.rounds) return;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = 128 * (wave & 1), wn = 64 * (wave >> 1);
+  const int lrow = lane & 15, q = lane >> 4;
+  const int nk = (int)((p.K + kKB - 1) / kKB);
+
+  // Copies: one instruction moves eight rows (lane i: row i / 8, LDS piece i % 8, which holds the row's piece
+  // i % 8 ^ swizzle).  Wave w copies LDS rows 32 w .. 32 w + 31 of A and of B, and the scales of rows
+  // 64 (w % 4) .. + 63 of A (w < 4) or B.
+  const int l8 = lane >> 3;
+  const int piece0 = ((lane & 7) ^ (l8 >> 1)) * 16, piece1 = ((lane & 7) ^ (4 + (l8 >> 1))) * 16;
+  const int brow = 16 * (l8 >> 2) + (l8 & 3);              // the lane's part of strip_col
+  const uint32_t dA = lds_addr(&sA[0][32 * wave * kKB]), dB = lds_addr(&sB[0][32 * wave * kKB]);
+  auto issue = [&](int tm, int tn, int kt, int st) {
+    const int64_t m0 = (int64_t)tm * kBT, n0 = (int64_t)tn * kBT;
+    const uint32_t ma = (uint32_t)(p.M - 1 - m0 < kBT ? p.M - 1 - m0 : kBT - 1);
+    const uint32_t na = (uint32_t)(p.N - 1 - n0 < kBT ? p.N - 1 - n0 : kBT - 1);
+    const uint8_t* a = uniform(p.a_codes + m0 * p.lda + (int64_t)kt * kKB);
+    const uint8_t* b = uniform(p.b_codes + n0 * p.ldb + (int64_t)kt * kKB);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // LDS row f = 32 w + 8 e + l8; of B it is column 64 (f / 64) + strip_col(f % 64)
+      const uint32_t ra = min((uint32_t)(32 * wave + 8 * e + l8), ma);
+      const int s8 = 4 * (wave & 1) + e;
+      const uint32_t rb = min((uint32_t)(64 * (wave >> 1) + 32 * (s8 & 1) + 4 * (s8 >> 1) + brow), na);
+      const uint32_t piece = (uint32_t)((e & 1) ? piece1 : piece0);
+      dma16(a, __umul24(ra, (uint32_t)p.lda) + piece, dA + st * kStage + e * 8 * kKB);
+      dma16(b, __umul24(rb, (uint32_t)p.ldb) + piece, dB + st * kStage + e * 8 * kKB);
+    }
+    const uint32_t f = (uint32_t)(64 * (wave & 3) + lane);
+    if (wave < 4) {
+      dma4(uniform(p.a_scales + (int64_t)kt * p.lda_scales + m0), 4 * min(f, ma), lds_addr(&sSA[st][64 * (wave & 3)]));
+    } else if constexpr (KIND == MX_FP8_LINE) {
+      dma4(uniform(p.b_scales + (int64_t)kt * p.ldb_scales + n0), 4 * min(f, na), lds_addr(&sSB[st][64 * (wave & 3)]));
+    } else if (wave == 4) {
+      // a tile's two scales, each for 128 columns: lanes 0 .. 31 copy the first, 32 .. 63 the second
+      const uint32_t last = (uint32_t)((p.N - 1) / kFp8Block), first = (uint32_t)(n0 / kFp8Block);
+      const uint32_t row = min(first + (uint32_t)(lane >> 5), last) - first;
+      dma4(uniform(p.b_scales + (int64_t)first * p.ldb_scales + kt), 4 * row * (uint32_t)p.ldb_scales,
+           lds_addr(&sSB[st][0]));
+    }
+  };
+
+  v4f acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  int nbm = 0, nbn = 0;
+  int rn = next_tile(map, r + 1, nbm, nbn);
+  issue(bm, bn, 0, 0);
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  if (nk > 1) issue(bm, bn, 1, 1);
+  else if (rn < map.rounds) issue(nbm, nbn, 0, 1);
+
+  v8i fb[4], fa[2];
+  float sa[8], sb[KIND == MX_FP8_LINE ? 16 : 1];
+  int st = 0;
+  // a fragment row's two pieces: their place depends on the lane only, rows 16 apart are immediates
+  const uint32_t off0 = lrow * kKB + ((2 * q) ^ (lrow >> 1)) * 16, off1 = lrow * kKB + ((2 * q + 1) ^ (lrow >> 1)) * 16;
+  auto read = [&](const uint8_t* base, int f) {
+    const u32x4 x = *(const u32x4*)(base + off0 + f * 16 * kKB), y = *(const u32x4*)(base + off1 + f * 16 * kKB);
+    return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+  };
+  auto read_scales = [&](int stage) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sa[i] = sSA[stage][wm + 16 * i + lrow];
+    if constexpr (KIND == MX_FP8_LINE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v4f x = *(const v4f*)&sSB[stage][wn + 16 * q + 4 * j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[4 * j + e] = x[e];
+      }
+    } else {
+      const float s = sSB[stage][(wn >> 7) * 32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sa[i] *= s;
+    }
+  };
+  auto join = [&](v4f& c, const v4f& d, int i, int j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = fmaf(d[e], KIND == MX_FP8_LINE ? sa[i] * sb[4 * j + e] : sa[i], c[e]);
+    // the sums have no use before the next step: without this they are sunk there, every product kept until then
+    asm volatile("" : "+v"(c));
+  };
+  auto mul = [&](const v8i& b, const v8i& a) {
+    Operand<false> x, y;
+    x.x = b;
+    y.x = a;
+    return mma<BF, AF, false>(x, y);
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) fb[j] = read(sB[0] + wn * kKB, j);
+  fa[0] = read(sA[0] + wm * kKB, 0);
+  read_scales(0);
+  for (;;) {
+    for (int kt = 0; kt < nk; ++kt) {
+      v4f d[2][4];
+      const uint8_t* a = sA[st] + wm * kKB;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        fa[(i + 1) & 1] = read(a, i + 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[i & 1][j] = mul(fb[j], fa[i & 1]);
+          if (i > 0) join(acc[i - 1][j], d[(i - 1) & 1][j], i - 1, j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // rows 6 and 7
+      fa[1] = read(a, 7);
+      const bool more = kt + 1 < nk || rn < map.rounds;
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (kt + 2 < nk) issue(bm, bn, kt + 2, st);
+      else if (rn < map.rounds && kt + 2 - nk < nk) issue(nbm, nbn, kt + 2 - nk, st);
+      st ^= 1;
+      const uint8_t* b = sB[st] + wn * kKB;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[0][j] = mul(fb[j], fa[0]);
+        join(acc[5][j], d[1][j], 5, j);
+        d[1][j] = mul(fb[j], fa[1]);
+        if (more) fb[j] = read(b, j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) fa[0] = read(sA[st] + wm * kKB, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        join(acc[6][j], d[0][j], 6, j);
+        join(acc[7][j], d[1][j], 7, j);
+      }
+      if (more) read_scales(st);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      store16<MX_OUT_BF16>(p, (int64_t)bm * kBT + wm + 16 * i + lrow, (int64_t)bn * kBT + wn + 16 * q, acc[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    if (rn >= map.rounds) break;
+    r = rn;
+    bm = nbm;
+    bn = nbn;
+    rn = next_tile(map, r + 1, nbm, nbn);
+  }
+}
+
+// The large-product kernel looks two steps ahead, so that K must span two blocks.  Its copies address a tile's rows by 32-bit offsets whose row pitch is a 24-bit factor.
+bool big_offsets(const Fp8GemmParams& p) {
+  const int64_t lim = int64_t(1) << 24;
+  return p.lda < lim && p.ldb < lim && p.lda_scales < lim && p.ldb_scales < lim && p.K < (int64_t(1) << 30);
 }
 
 template <int AF, int BF, int KIND, int OUT>
 void launch(const Fp8GemmParams& p, hipStream_t s) {
+  if constexpr (OUT == MX_OUT_BF16) {
+    if (p.M >= kBT && p.N >= kBT && p.K > kKB && big_offsets(p)) {
+      BigMap map;
+      map.tiles_m = (int)((p.M + kBT - 1) / kBT);
+      map.tiles_n = (int)((p.N + kBT - 1) / kBT);
+      map.groups_m = (map.tiles_m + kGroupM - 1) / kGroupM;
+      map.groups = map.groups_m * ((map.tiles_n + kGroupN - 1) / kGroupN);
+      map.rounds = (map.groups + kXcds - 1) / kXcds;
+      hipLaunchKernelGGL((fp8_mm_big<AF, BF, KIND>), dim3(kXcds * kGroupM * kGroupN), dim3(kBThreads), 0, s, p, map);
+      return;
+    }
+  }
   const int64_t tm = (p.M + kGT - 1) / kGT, tn = (p.N + kGT - 1) / kGT;
-  hipLaunchKernelGGL((fp8_mm_any<AF, BF, KIND, OUT>), dim3((unsigned)(tm * tn)), dim3(kGThreads), 0, s, p, tm,
-                     wide_rows(p, OUT));
+  hipLaunchKernelGGL((fp8_mm_any<AF, BF, KIND, OUT>), dim3((unsigned)(tm * tn)), dim3(kGThreads), 0, s, p, tm);
 }
 
 template <int AF, int BF>

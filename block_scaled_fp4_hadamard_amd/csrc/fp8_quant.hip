@@ -2,7 +2,7 @@
 // per line and 128 values (LINE), or per 128 x 128 tile (TILE), along the rows
 // of a bf16 matrix, its columns (the transpose's lines), or both from one read.
 //
-//   s = max(RN(amax / F), 2^-126), F = 448 (E4M3) or 57344 (E5M2)
+//   s = max(RN(amax * RN(1 / F)), 2^-126), F = 448 (E4M3) or 57344 (E5M2)
 //   r = RN(1 / s), code = RNE8(RN(x * r))
 //
 // x * r stays within F (1 + 2^-22), which rounds to F, so nothing saturates.
@@ -58,7 +58,7 @@ template <int FMT>
 __device__ __forceinline__ void block_scale(uint32_t mag, float& s, float& r) {
   constexpr float kLargest = FMT == MX_FP8_E4M3 ? 448.0f : 57344.0f;
   const bool bad = mag >= 0x7F80u;
-  s = fmaxf(__uint_as_float(mag << 16) / kLargest, 0x1p-126f);
+  s = fmaxf(__uint_as_float(mag << 16) * (1.0f / kLargest), 0x1p-126f);
   r = 1.0f / s;
   if (bad) {
     s = __uint_as_float(0x7FC00000u);

@@ -381,7 +381,7 @@ typedef struct {
 /*
  * mx_fp8_quantize: the 8-bit cast of a bf16 matrix.  Per block (a line's 128
  * values, or a 128 x 128 tile; the last ones of an axis may be part-filled):
- *   s = max(RN32(amax / F), 2^-126), F = 448 or 57344;  r = RN32(1 / s);
+ *   s = max(RN32(amax * RN32(1 / F)), 2^-126), F = 448 or 57344;  r = RN32(1 / s);
  *   code = RN32(x * r) rounded to nearest even in the format.
  * A block holding Inf or NaN gets s = NaN and codes 0.
  *   x, rows, cols, ld_x  device, 16-byte aligned bf16 bit patterns; any rows,
@@ -436,7 +436,7 @@ mx_status mx_fp8_gemm(const mx_fp8_tensor *a, mx_fp8_fmt a_fmt, const mx_fp8_ten
  * cast after it:
  *   m  E4M3, F = 448;  v  E5M3 (unsigned: 5 exponent and 3 mantissa bits, a
  *   float16's bits 14..7, codes to 0xF7), F = 61440;
- *   s = max(RN32(amax / F), 2^-126), y = RN32(value * RN32(1 / s)) rounded by
+ *   s = max(RN32(amax * RN32(1 / F)), 2^-126), y = RN32(value * RN32(1 / s)) by
  *   MX_ROUND_RTNE or stochastically as mx_quantize rounds (16-bit draws;
  *   element i of tensor k takes stream 4 + 2k for m, 5 + 2k for v, key seed);
  *   a v above 0 keeps at least code 1; a block of m or v holding Inf or NaN

@@ -3,9 +3,9 @@
 Test infrastructure only: see the package docstring.
 
 A block is 128 consecutive values of a line ("line") or 128 lines x 128 values ("tile"); the last blocks of an axis
-may be part-filled.  s = max(RN32(amax / F), 2^-126), r = RN32(1 / s), y = RN32(x * r), and the code is y rounded to
-nearest, ties to the even code, in E4M3 (finite, largest 448) or E5M2 (largest finite 57344).  A block holding Inf or
-NaN has s = NaN and codes 0.
+may be part-filled.  s = max(RN32(amax * RN32(1 / F)), 2^-126), r = RN32(1 / s), y = RN32(x * r), and the code is y
+rounded to nearest, ties to the even code, in E4M3 (finite, largest 448) or E5M2 (largest finite 57344).  A block
+holding Inf or NaN has s = NaN and codes 0.
 
 The rounding is a nearest-level search over the table of all finite magnitudes, built from the bit fields.
 """
@@ -45,7 +45,7 @@ def bf16_values(bits):
 def scales_of(amax, largest):
     """s and r = RN32(1 / s) of each block's float32 amax (NaN or Inf: s = NaN, r = 0)."""
     with np.errstate(all="ignore"):
-        s = np.maximum(amax / np.float32(largest), np.float32(2.0 ** -126)).astype(np.float32)
+        s = np.maximum(amax * (np.float32(1) / np.float32(largest)), np.float32(2.0 ** -126)).astype(np.float32)
         r = (np.float32(1.0) / s).astype(np.float32)
     bad = ~np.isfinite(amax)
     return np.where(bad, np.float32(np.nan), s), np.where(bad, np.float32(0), r)

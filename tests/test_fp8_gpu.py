@@ -146,7 +146,8 @@ def test_bf16_output_on_normal_data():
 SHAPES = [(1, 1, 1), (1, 16, 128), (1, 1000, 300), (2, 130, 129), (5, 4096, 512), (15, 129, 4000), (16, 512, 1024),
           (17, 65, 257), (31, 1003, 640), (33, 300, 1000), (64, 256, 14336), (65, 500, 384), (100, 1, 700),
           (128, 128, 128), (129, 127, 255), (255, 257, 600), (256, 256, 256), (300, 1003, 1001), (512, 768, 640),
-          (700, 520, 2000), (1000, 1300, 385)]
+          (700, 520, 2000), (1000, 1300, 385),
+          (4200, 4300, 300)]
 
 
 @pytest.mark.parametrize("kind", ["line", "tile"])

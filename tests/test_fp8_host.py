@@ -122,7 +122,7 @@ def test_state_codes():
         # mean of n draws of a variable within one step: six standard deviations of at most step / (2 sqrt n)
         assert np.all(np.abs(total / n - x)[big] <= (6 / (2 * math.sqrt(n)) + 2.0 ** -16) * step[big])
     codes, s = adamw.encode_state(np.array([np.inf] + [1.0] * 200, np.float32), False)
-    assert np.isnan(s[0]) and s[1] == np.float32(1.0) / np.float32(61440) and not codes[:128].any() and codes[128] == 0xF7
+    assert np.isnan(s[0]) and s[1] == np.float32(1 / 61440) and not codes[:128].any() and codes[128] == 0xF7
 
 
 # ---- refusals of the C entries

@@ -32,6 +32,7 @@
 // them without any exchange between lanes.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <utility>
 #include "fp8_kernels.h"
 
 namespace mx {
@@ -52,6 +53,16 @@ constexpr int kKB = 128;      // bytes (values) of a row per K step
 // 2 (l / 16) and 2 (l / 16) + 1 instead met every bank twice (45% of the LDS
 // cycles of the large kernel).
 __device__ __forceinline__ int slot(int row, int piece) { return (piece ^ ((row >> 1) & 7)) * 16; }
+
+// f(0), f(1), ... f(N - 1), each index a constant of its own instance
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(const F& f) {
+  each(std::make_integer_sequence<int, N>{}, f);
+}
 
 // the strip column that row f of the strip's LDS rows holds (fragment order)
 __device__ __forceinline__ int strip_col(int f) { return 16 * ((f >> 2) & 3) + 4 * (f >> 4) + (f & 3); }
@@ -133,34 +144,55 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef v4f v4f_any __attribute__((aligned(4)));
 
-// Sixteen consecutive columns of one row of C from a lane's accumulators.  Non-temporal: the output streams
-// past the L2, which keeps the operand rows that the next tiles read.
+// A wave's 16 rows x 64 columns of C from its accumulators: row m0 + l % 16, columns n0 + 16 (l / 16) .. + 15 in
+// lane l.  Non-temporal: the output streams past the L2, which keeps the operand rows that the next tiles read.
+// bf16: lanes l and l ^ 8 trade halves of their 32 bytes, so that each store writes whole 128-byte pieces of
+// eight rows.  The last columns of an odd width go one by one.
 template <int OUT>
-__device__ __forceinline__ void store16(const Fp8GemmParams& p, int64_t m, int64_t n, const v4f (&acc)[4]) {
-  if (m >= p.M || n >= p.N) return;
-  const int64_t at = m * p.ldc + n;
-  if (n + 16 <= p.N) {
-    if constexpr (OUT == MX_OUT_F32) {
+__device__ __forceinline__ void store_rows(const Fp8GemmParams& p, int64_t m0, int64_t n0, int lane,
+                                           const v4f (&acc)[4]) {
+  const int lrow = lane & 15, q = lane >> 4;
+  if constexpr (OUT == MX_OUT_F32) {
+    const int64_t m = m0 + lrow, n = n0 + 16 * q;
+    if (m >= p.M) return;
+    float* c = (float*)p.c + m * p.ldc + n;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) __builtin_nontemporal_store(acc[j], (v4f_any*)((float*)p.c + at + 4 * j));
-    } else {
+    for (int j = 0; j < 4; ++j) {
+      if (n + 4 * j + 4 <= p.N) {
+        __builtin_nontemporal_store(acc[j], (v4f_any*)(c + 4 * j));
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        __builtin_nontemporal_store(
-            u32x4{pack_bf16(acc[2 * h][0], acc[2 * h][1]), pack_bf16(acc[2 * h][2], acc[2 * h][3]),
-                  pack_bf16(acc[2 * h + 1][0], acc[2 * h + 1][1]), pack_bf16(acc[2 * h + 1][2], acc[2 * h + 1][3])},
-            (u32x4_any*)((uint16_t*)p.c + at + 8 * h));
+        for (int r = 0; r < 4; ++r)
+          if (n + 4 * j + r < p.N) c[4 * j + r] = acc[j][r];
+      }
     }
-    return;
+  } else {
+    u32x4 h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      h[e] = u32x4{pack_bf16(acc[2 * e][0], acc[2 * e][1]), pack_bf16(acc[2 * e][2], acc[2 * e][3]),
+                   pack_bf16(acc[2 * e + 1][0], acc[2 * e + 1][1]), pack_bf16(acc[2 * e + 1][2], acc[2 * e + 1][3])};
+    const bool low = lrow < 8;
+    u32x4 got;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      got[e] = (uint32_t)__builtin_amdgcn_mov_dpp((int)(low ? h[1][e] : h[0][e]), 0x128, 0xF, 0xF, false);   // l ^ 8
+    const int64_t n = n0 + 16 * q + 8 * (lrow >> 3);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t m = m0 + (lrow & 7) + 8 * e;
+      const u32x4 x = low == (e == 0) ? h[e] : got;
+      if (m >= p.M) continue;
+      uint16_t* c = (uint16_t*)p.c + m * p.ldc + n;
+      if (n + 8 <= p.N) {
+        __builtin_nontemporal_store(x, (u32x4_any*)c);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (n + r < p.N) c[r] = (uint16_t)(x[r >> 1] >> (16 * (r & 1)));
+      }
+    }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (n + 4 * j + r >= p.N) return;
-      if constexpr (OUT == MX_OUT_F32) ((float*)p.c)[at + 4 * j + r] = acc[j][r];
-      else ((uint16_t*)p.c)[at + 4 * j + r] = (uint16_t)pack_bf16(acc[j][r], 0.0f);
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -231,7 +263,7 @@ __global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, i
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) store16<OUT>(p, m0 + wm + 16 * i + lrow, col, acc[i]);
+  for (int i = 0; i < 4; ++i) store_rows<OUT>(p, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
 }
 
 // ---------------------------------------------------------------------------
@@ -240,12 +272,17 @@ __global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, i
 // one block (a 128-byte line of every operand row) per step, copied global ->
 // LDS by DMA into one of two 64 KB stages while the other is consumed.
 //
-// A wave holds the step's four B fragments and streams its eight A fragments;
-// row i's four matrix instructions run beside the fused multiply-adds of row
-// i - 1, so their results are never waited for.  The step's last two rows run
-// column by column after the barrier that frees the stage: a B fragment is
-// replaced by the next step's as soon as its two instructions are issued, which
-// hides the next step's first LDS reads behind the last quarter of this one.
+// A wave's step is 32 matrix instructions (eight A fragments x four B
+// fragments), and each runs beside the four multiply-adds that join the result
+// of four instructions earlier, so that nothing waits for a result.  Rows 0 - 4
+// run row by row, each A fragment read three rows ahead; then every read of
+// the stage is done, and a barrier frees it for the copies of the step after
+// next.  Rows 5 - 7 run column by column behind the barrier, so that a B
+// fragment is free after its three instructions and the next step's can be
+// read: the next step's first LDS reads hide behind the last three eighths of
+// this one.  (The two waves of a SIMD do not share its matrix core evenly: the
+// older one runs ahead, and the younger finishes the step alone, when only its
+// own reads ahead cover the LDS latency.)
 //
 // Rows of a tile past the operand's last line read that line again (their
 // results are not stored), so every copy stays inside the operand and any M
@@ -290,6 +327,10 @@ __device__ __forceinline__ int next_tile(const BigMap& t, int r, int& bm, int& b
   return t.rounds;
 }
 
+// the step's order: instruction n works on fragment row row_of(n) and column col_of(n)
+__device__ constexpr int row_of(int n) { return n < 20 ? n / 4 : 5 + (n - 20) % 3; }
+__device__ constexpr int col_of(int n) { return n < 20 ? n % 4 : (n - 20) / 3; }
+
 template <int AF, int BF, int KIND>
 __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p, const BigMap map) {
   __shared__ __attribute__((aligned(1024))) uint8_t sA[2][kStage], sB[2][kStage];
@@ -332,11 +373,14 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
   auto copy = [&](int st) {
     const uint32_t a0 = dA + st * kStage, b0 = dB + st * kStage;
     if (!edge) {
+      // the pitches are made opaque, so that their multiples are formed here and not kept in registers
+      uint32_t pa = (uint32_t)p.lda, pb = (uint32_t)p.ldb;
+      asm volatile("" : "+s"(pa), "+s"(pb));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         // rows 8 e .. 8 e + 7 of A; of B the strip columns of these LDS rows
-        dma16(ca + (uint32_t)(8 * e) * (uint32_t)p.lda, (e & 1) ? la1 : la0, a0 + e * 8 * kKB);
-        dma16(cb + (uint32_t)(32 * (e & 1) + 4 * (e >> 1)) * (uint32_t)p.ldb, (e & 1) ? lb1 : lb0, b0 + e * 8 * kKB);
+        dma16(ca + (uint32_t)(8 * e) * pa, (e & 1) ? la1 : la0, a0 + e * 8 * kKB);
+        dma16(cb + (uint32_t)(32 * (e & 1) + 4 * (e >> 1)) * pb, (e & 1) ? lb1 : lb0, b0 + e * 8 * kKB);
       }
     } else {
 #pragma unroll
@@ -391,8 +435,8 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
   issue(1);
 
-  v8i fb[4], fa[2];
-  float sa[3], sb[KIND == MX_FP8_LINE ? 16 : 1];
+  v8i fb[4], fa[4];          // fragment row i in fa[i % 4]
+  float sb[KIND == MX_FP8_LINE ? 16 : 1];
   int st = 0;
   // a fragment row's two pieces: their place depends on the lane only, rows 16 apart are immediates
   const uint32_t off0 = lrow * kKB + slot(lrow, q), off1 = lrow * kKB + slot(lrow, q + 4);
@@ -400,9 +444,6 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
     const u32x4 x = *(const u32x4*)(base + off0 + f * 16 * kKB), y = *(const u32x4*)(base + off1 + f * 16 * kKB);
     return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
-  // row i's A scale, read with its fragment and used (times the tile's scale) one row later
-  auto read_sa = [&](int stage, int i) { sa[i % 3] = sSA[stage][wm + 16 * i + lrow]; };
-  auto row_scale = [&](int i) { return KIND == MX_FP8_LINE ? sa[i % 3] : sa[i % 3] * sb[0]; };
   auto read_sb = [&](int stage) {
     if constexpr (KIND == MX_FP8_LINE) {
 #pragma unroll
@@ -427,63 +468,75 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
     y.x = a;
     return mma<BF, AF, false>(x, y);
   };
+  // Instruction n's result stays in d[n % 4] until instruction n + 4 is due.  A step's last four results are joined
+  // in the next step (tile scales), or at its end (line scales, whose columns' scales the next step replaces).
+  constexpr bool kCarry = KIND == MX_FP8_TILE;
+  v4f d[4];
+  float carry[3];                // the scales of rows 5 - 7 of the step before
+  auto clear = [&]() {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) d[n] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 3; ++n) carry[n] = 0.0f;
+  };
+  clear();
 #pragma unroll
   for (int j = 0; j < 4; ++j) fb[j] = read(sB[0] + wn * kKB, j);
-  fa[0] = read(sA[0] + wm * kKB, 0);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) fa[i] = read(sA[0] + wm * kKB, i);
   read_sb(0);
-  read_sa(0, 0);
   for (;;) {
     for (int kt = 0; kt < nk; ++kt) {
-      v4f d[2][4];
-      const uint8_t* a = sA[st] + wm * kKB;
+      float s[8];
+      each<32>([&](auto index) {
+        constexpr int n = decltype(index)::value, i = row_of(n), j = col_of(n);
+        if constexpr (n < 20 && j == 0) {
+          s[i] = sSA[st][wm + 16 * i + lrow];
+          if constexpr (i == 4) {
 #pragma unroll
-      for (int i = 0; i < 6; ++i) {
-        fa[(i + 1) & 1] = read(a, i + 1);
-        read_sa(st, i + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          d[i & 1][j] = mul(fb[j], fa[i & 1]);
-          if (i > 0) {
-            if (j == 0) s = row_scale(i - 1);
-            join(acc[i - 1][j], d[(i - 1) & 1][j], s, j);
+            for (int e = 5; e < 8; ++e) s[e] = sSA[st][wm + 16 * e + lrow];
           }
+          fa[(i + 3) & 3] = read(sA[st] + wm * kKB, i + 3);
           __builtin_amdgcn_sched_barrier(0);
         }
-      }
-      // rows 6 and 7
-      fa[1] = read(a, 7);
-      read_sa(st, 7);
-      const bool more = kt + 1 < nk || rn < map.rounds;
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      issue(st);
-      st ^= 1;
-      const uint8_t* b = sB[st] + wn * kKB;
-      const float s5 = row_scale(5), s6 = row_scale(6), s7 = row_scale(7);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[0][j] = mul(fb[j], fa[0]);
-        join(acc[5][j], d[1][j], s5, j);
-        d[1][j] = mul(fb[j], fa[1]);
-        if (more) fb[j] = read(b, j);
+        if constexpr (n == 20) {
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          issue(st);
+          st ^= 1;
+          fa[0] = read(sA[st] + wm * kKB, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (n >= 4) {
+          constexpr int mi = row_of(n - 4), mj = col_of(n - 4);
+          if constexpr (KIND == MX_FP8_TILE && mj == 0) s[mi] *= sb[0];
+          join(acc[mi][mj], d[n & 3], s[mi], mj);
+        } else if constexpr (kCarry) {
+          join(acc[row_of(28 + n)][col_of(28 + n)], d[n], carry[row_of(28 + n) - 5], 0);
+        }
+        d[n & 3] = mul(fb[j], fa[i & 3]);
+        if constexpr (n >= 20 && i == 7) fb[j] = read(sB[st] + wn * kKB, j);
+        if constexpr (n == 29) fa[1] = read(sA[st] + wm * kKB, 1);
+        if constexpr (n == 30) fa[2] = read(sA[st] + wm * kKB, 2);
         __builtin_amdgcn_sched_barrier(0);
-      }
-      if (more) fa[0] = read(sA[st] + wm * kKB, 0);
+      });
+      if constexpr (kCarry) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        join(acc[6][j], d[0][j], s6, j);
-        join(acc[7][j], d[1][j], s7, j);
+        for (int e = 0; e < 3; ++e) carry[e] = s[5 + e];
+      } else {
+#pragma unroll
+        for (int n = 28; n < 32; ++n) join(acc[row_of(n)][col_of(n)], d[n & 3], s[row_of(n)], col_of(n));
       }
-      if (more) {
-        read_sb(st);
-        read_sa(st, 0);
-      }
+      read_sb(st);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kCarry) {
+#pragma unroll
+      for (int n = 28; n < 32; ++n) join(acc[row_of(n)][col_of(n)], d[n & 3], carry[row_of(n) - 5], 0);
+      clear();
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      store16<MX_OUT_BF16>(p, (int64_t)bm * kBT + wm + 16 * i + lrow, (int64_t)bn * kBT + wn + 16 * q, acc[i]);
+      store_rows<MX_OUT_BF16>(p, (int64_t)bm * kBT + wm + 16 * i, (int64_t)bn * kBT + wn, lane, acc[i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }

@@ -21,7 +21,7 @@ FP8_KIND = {"line": 0, "tile": 1}
 
 EXPORTS = ("mx_quantize", "mx_hadamard_quantize", "mx_gemm", "mx_gemm_grouped", "mx_mxnorm_quantize", "mx_quant_stats",
            "mx_nvfp4_quantize", "mx_hadamard_rotate", "mx_quantize_f32", "mx_osci_reset", "mx_fp8_quantize",
-           "mx_fp8_gemm", "mx_adamw_step", "mx_status_str", "mx_version")
+           "mx_fp8_gemm", "mx_fp8_gemm_workspace", "mx_adamw_step", "mx_status_str", "mx_version")
 
 
 class MXError(RuntimeError):
@@ -102,8 +102,10 @@ def lib():
         fp = ctypes.POINTER(Fp8TensorC)
         L.mx_fp8_quantize.argtypes = [vp, i64, i64, i64, i32, i32, i32, fp, fp, vp]
         L.mx_fp8_quantize.restype = ctypes.c_int
-        L.mx_fp8_gemm.argtypes = [fp, i32, fp, i32, i32, i64, i64, i64, vp, i64, i32, vp]
+        L.mx_fp8_gemm.argtypes = [fp, i32, fp, i32, i32, i64, i64, i64, vp, i64, i32, vp, i64, vp]
         L.mx_fp8_gemm.restype = ctypes.c_int
+        L.mx_fp8_gemm_workspace.argtypes = [i64, i64, i64, i32]
+        L.mx_fp8_gemm_workspace.restype = i64
         L.mx_adamw_step.argtypes = [ctypes.POINTER(AdamwTensorC), i32, i32, ctypes.POINTER(AdamwParamsC), i32, u64, vp]
         L.mx_adamw_step.restype = ctypes.c_int
         L.mx_status_str.argtypes = [ctypes.c_int]
@@ -197,9 +199,13 @@ def mx_fp8_quantize(x_ptr, rows, cols, ld_x, fmt, kind, axis, row_q, col_q, stre
                                  ctypes.byref(col_q) if col_q is not None else None, stream)
 
 
-def mx_fp8_gemm(a_q, a_fmt, b_q, b_fmt, b_kind, M, N, K, c_ptr, ldc, out, stream):
+def mx_fp8_gemm(a_q, a_fmt, b_q, b_fmt, b_kind, M, N, K, c_ptr, ldc, out, workspace, workspace_bytes, stream):
     return lib().mx_fp8_gemm(ctypes.byref(a_q), a_fmt, ctypes.byref(b_q), b_fmt, b_kind, M, N, K, c_ptr, ldc, out,
-                             stream)
+                             workspace, workspace_bytes, stream)
+
+
+def mx_fp8_gemm_workspace(M, N, K, out):
+    return lib().mx_fp8_gemm_workspace(M, N, K, out)
 
 
 def mx_adamw_step(tensors, count, bits, params, rnd, seed, stream):

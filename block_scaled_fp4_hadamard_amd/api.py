@@ -440,11 +440,14 @@ def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
         raise ValueError("the output must be float32 or bfloat16, got %s" % out.dtype)
     if b.codes.device != dev or out.device != dev:
         raise ValueError("a, b and out must be on one device")
-    kind = "f32" if out.dtype == torch.float32 else "bf16"
+    kind = _lib.OUT["f32" if out.dtype == torch.float32 else "bf16"]
     with _launch_on(dev):
+        # the workspace is this call's own: the allocator gives its memory to later work of the same stream only
+        size = _lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
+        space = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
         st = _lib.mx_fp8_gemm(a.c_struct(), _lib.FP8_FMT[a.fmt], b.c_struct(), _lib.FP8_FMT[b.fmt],
-                              _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), _pitch(out, "out"),
-                              _lib.OUT[kind], _stream(dev))
+                              _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), _pitch(out, "out"), kind,
+                              space.data_ptr() if size else None, size, _stream(dev))
     _lib.check(st, "mx_fp8_gemm")
     return out
 

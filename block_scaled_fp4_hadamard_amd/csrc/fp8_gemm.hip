@@ -67,12 +67,6 @@ __device__ __forceinline__ void each(const F& f) {
 // the strip column that row f of the strip's LDS rows holds (fragment order)
 __device__ __forceinline__ int strip_col(int f) { return 16 * ((f >> 2) & 3) + 4 * (f >> 4) + (f & 3); }
 
-__device__ __forceinline__ v8i fragment(const uint8_t* lds, int row, int q) {
-  const u32x4 x = *(const u32x4*)(lds + row * kKB + slot(row, q));
-  const u32x4 y = *(const u32x4*)(lds + row * kKB + slot(row, q + 4));
-  return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
-}
-
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -195,75 +189,325 @@ __device__ __forceinline__ void store_rows(const Fp8GemmParams& p, int64_t m0, i
   }
 }
 
+constexpr int kXcds = 8;
+
+// Global -> LDS copy of 16 (4) bytes per lane: LDS address = M0 + size * lane.  Inline asm, so that the
+// compiler places no waits of its own for it; it writes no register.  An SALU write of M0 needs one wait
+// state before the copy reads it.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const T*)(((uint64_t)hi << 32) | lo);
+}
+
 // ---------------------------------------------------------------------------
-// Bounds-checked kernel, any shape: a 128 x 128 tile of C per workgroup, four
-// waves of 64 x 64, operands through registers into LDS one K block at a time.
-constexpr int kGT = 128, kGThreads = 256;
+// Few rows of A (single tokens and short batches): the operand that matters is
+// B, read once from HBM.  A workgroup takes 16 J columns of C and all M <= 16 F
+// rows; its waves take the K blocks in turn, straight from memory to registers
+// with U blocks in flight, and their sums meet in LDS in the waves' order.
+// Rows past M and columns past N read the last one and are not stored.
+constexpr int kFewWaves = 8;
+
+template <int AF, int BF, int KIND, int OUT, int F, int J>
+__global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams p) {
+  constexpr bool kExact = OUT == MX_OUT_F32;
+  constexpr int U = F == 1 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) v4f part[kFewWaves][F * J][64];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int lrow = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * J;
+  const int64_t nk = (p.K + kKB - 1) / kKB;
+  const uint8_t *a[F], *b[J];
+  const float *sa[F], *sb[J];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int64_t m = 16 * f + lrow < p.M ? 16 * f + lrow : p.M - 1;
+    a[f] = p.a_codes + m * p.lda + q * 16;
+    sa[f] = p.a_scales + m;
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int64_t n = n0 + 16 * j + lrow < p.N ? n0 + 16 * j + lrow : p.N - 1;
+    b[j] = p.b_codes + n * p.ldb + q * 16;
+    // a lane's accumulators are columns 4 q .. 4 q + 3 of the fragment
+    const int64_t c = n0 + 16 * j < p.N ? n0 + 16 * j : p.N - 1;
+    sb[j] = KIND == MX_FP8_LINE ? p.b_scales : p.b_scales + (c / kFp8Block) * p.ldb_scales;
+  }
+  auto piece2 = [](const uint8_t* x) {
+    const u32x4 u = *(const u32x4*)x, v = *(const u32x4*)(x + 64);
+    return v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+  };
+  v4f acc[F][J];
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[f][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int64_t kb = wave; kb < nk; kb += kFewWaves * U) {
+    v8i ra[U][F], rb[U][J];
+    float ca[U][F];
+    v4f cb[U][J];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a block past the last reads the last again and counts nothing
+      const int64_t k = kb + u * kFewWaves < nk ? kb + u * kFewWaves : nk - 1;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        rb[u][j] = piece2(b[j] + k * kKB);
+        if constexpr (KIND == MX_FP8_TILE) {
+          cb[u][j][0] = sb[j][k];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t c = n0 + 16 * j + 4 * q + r;
+            cb[u][j][r] = sb[j][k * p.ldb_scales + (c < p.N ? c : p.N - 1)];
+          }
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        ra[u][f] = piece2(a[f] + k * kKB);
+        ca[u][f] = sa[f][k * p.lda_scales];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool counts = kb + u * kFewWaves < nk;
+      Operand<kExact> ob[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) ob[j] = operand<BF, kExact>(rb[u][j]);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const Operand<kExact> oa = operand<AF, kExact>(ra[u][f]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const v4f d = mma<BF, AF, kExact>(ob[j], oa);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float s = ca[u][f] * cb[u][j][KIND == MX_FP8_TILE ? 0 : r];
+            acc[f][j][r] = fmaf(d[r], counts ? s : 0.0f, acc[f][j][r]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int j = 0; j < J; ++j) part[wave][f * J + j][lane] = acc[f][j];
+  __syncthreads();
+  if (wave >= F * J) return;
+  v4f sum = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < kFewWaves; ++w) sum += part[w][wave][lane];
+  const int64_t m = 16 * (wave / J) + lrow, n = n0 + 16 * (wave % J) + 4 * q;
+  if (m >= p.M) return;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n + r < p.N) {
+      if constexpr (kExact) ((float*)p.c)[m * p.ldc + n + r] = sum[r];
+      else ((uint16_t*)p.c)[m * p.ldc + n + r] = (uint16_t)pack_bf16(sum[r], 0.0f);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Everything between, and fp32 output: a 128 x 128 tile of C per workgroup,
+// four waves of 64 x 64, two workgroups on a CU.  K blocks arrive by DMA in two
+// 32 KB LDS stages, as in the large kernel below; a step's 16 fragment
+// products run row by row, each joined four products later, and the barrier
+// that frees the stage comes before the last row.  Where tiles alone do not
+// fill the chip, a tile's K blocks are dealt to `splits` workgroups, whose
+// float32 sums go to the workspace and are added in order by a second launch.
+// Rows of a tile past the operand's last line read that line again.
+constexpr int kMT = 128, kMThreads = 256, kMStage = kMT * kKB;
+
+struct MidMap {
+  int tiles_m, tiles_n, splits, total, per_xcd;    // total = tiles_m * tiles_n * splits
+  float* parts;                                    // [splits][M][N] where splits > 1
+};
 
 template <int AF, int BF, int KIND, int OUT>
-__global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, int64_t tiles_m) {
-  __shared__ __attribute__((aligned(16))) uint8_t sA[kGT * kKB], sB[kGT * kKB];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int64_t m0 = (blockIdx.x % tiles_m) * kGT, n0 = (blockIdx.x / tiles_m) * kGT;
-  const int wm = 64 * (wave & 1), wn = 64 * (wave >> 1);
-  const int64_t nk = (p.K + kKB - 1) / kKB;
-  const int lrow = lane & 15, q = lane >> 4;
+__global__ void __launch_bounds__(kMThreads, 2) fp8_mm_mid(const Fp8GemmParams p, const MidMap map) {
+  constexpr bool kExact = OUT == MX_OUT_F32;
+  __shared__ __attribute__((aligned(1024))) uint8_t sA[2][kMStage], sB[2][kMStage];
+  __shared__ __attribute__((aligned(1024))) float sSA[2][kMT], sSB[2][kMT];
+  // an XCD (workgroup ids are dealt to them in turn) takes a contiguous run of tiles: split by split, bands of
+  // eight tile rows, column by column
+  const int id = (int)(blockIdx.x % kXcds) * map.per_xcd + (int)(blockIdx.x / kXcds);
+  if ((int)(blockIdx.x / kXcds) >= map.per_xcd || id >= map.total) return;
+  const int tiles = map.tiles_m * map.tiles_n, split = id / tiles, tile = id % tiles;
+  const int band = tile / (8 * map.tiles_n), in = tile % (8 * map.tiles_n);
+  const int rows = min(8, map.tiles_m - 8 * band);
+  const int64_t m0 = (int64_t)(8 * band + in % rows) * kMT, n0 = (int64_t)(in / rows) * kMT;
+  const int nkb = (int)((p.K + kKB - 1) / kKB);
+  const int k0 = (int)((int64_t)nkb * split / map.splits), k1 = (int)((int64_t)nkb * (split + 1) / map.splits);
 
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = 64 * (wave & 1), wn = 64 * (wave >> 1);
+  const int lrow = lane & 15, q = lane >> 4, l8 = lane >> 3;
+  const int64_t ma = p.M - 1 - m0 < kMT ? p.M - 1 - m0 : kMT - 1, na = p.N - 1 - n0 < kMT ? p.N - 1 - n0 : kMT - 1;
+  // wave w copies LDS rows 32 w .. 32 w + 31 of both operands, eight rows an instruction
+  uint32_t oa[4], ob[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int row = 32 * wave + 8 * e + l8;
+    const uint32_t piece = (uint32_t)slot(row, lane & 7);
+    oa[e] = (uint32_t)(row < ma ? row : ma) * (uint32_t)p.lda + piece;
+    const int col = (row & 64) + strip_col(row & 63);
+    ob[e] = (uint32_t)(col < na ? col : na) * (uint32_t)p.ldb + piece;
+  }
+  const int sr = 64 * (wave & 1) + lane;
+  const uint32_t os = 4u * (uint32_t)(wave < 2 ? (sr < ma ? sr : ma) : (KIND == MX_FP8_LINE ? (sr < na ? sr : na) : 0));
+  const uint8_t* ca = uniform(p.a_codes + m0 * p.lda + (int64_t)k0 * kKB);
+  const uint8_t* cb = uniform(p.b_codes + n0 * p.ldb + (int64_t)k0 * kKB);
+  const int64_t step = wave < 2 ? p.lda_scales : (KIND == MX_FP8_LINE ? p.ldb_scales : 1);
+  const float* cs = uniform(wave < 2 ? p.a_scales + k0 * p.lda_scales + m0
+                                     : (KIND == MX_FP8_LINE ? p.b_scales + k0 * p.ldb_scales + n0
+                                                            : p.b_scales + (n0 / kFp8Block) * p.ldb_scales + k0));
+  const uint32_t dA = lds_addr(&sA[0][32 * wave * kKB]), dB = lds_addr(&sB[0][32 * wave * kKB]);
+  const uint32_t dS = lds_addr(wave < 2 ? &sSA[0][64 * wave] : &sSB[0][64 * (wave & 1)]);
+  auto issue = [&](int st) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      dma16(ca, oa[e], dA + st * kMStage + e * 8 * kKB);
+      dma16(cb, ob[e], dB + st * kMStage + e * 8 * kKB);
+    }
+    dma4(cs, os, dS + st * kMT * 4);
+    ca += kKB;
+    cb += kKB;
+    cs += step;
+  };
+
+  const uint32_t off0 = lrow * kKB + slot(lrow, q), off1 = lrow * kKB + slot(lrow, q + 4);
+  auto read = [&](const uint8_t* base, int f) {
+    const u32x4 x = *(const u32x4*)(base + off0 + f * 16 * kKB), y = *(const u32x4*)(base + off1 + f * 16 * kKB);
+    return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+  };
+  float sb[KIND == MX_FP8_LINE ? 16 : 1];
+  auto read_sb = [&](int stage) {
+    if constexpr (KIND == MX_FP8_LINE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v4f x = *(const v4f*)&sSB[stage][wn + 16 * q + 4 * j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[4 * j + e] = x[e];
+      }
+    } else {
+      sb[0] = sSB[stage][0];
+    }
+  };
   v4f acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto join = [&](v4f& c, const v4f& d, float s, int j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = fmaf(d[e], KIND == MX_FP8_LINE ? s * sb[4 * j + e] : s, c[e]);
+    asm volatile("" : "+v"(c));      // kept here, not sunk to the next step
+  };
 
-  const int64_t col = n0 + wn + 16 * q;      // the lane's first column of C
-  for (int64_t kb = 0; kb < nk; ++kb) {
-    u32x4 ra[4], rb[4];
+  const int nk = k1 - k0;
+  issue(0);
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  if (nk > 1) issue(1);
+  int st = 0;
+  // A fragment row i in fa[i], B fragments as read; the widened form leaves no registers for row 3's own place,
+  // which row 0, widened by then, gives up
+  constexpr int kRow3 = kExact ? 0 : 3;
+  v8i fa[kExact ? 3 : 4], rb[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = 32 * e + (t >> 3), piece = t & 7;
-      const int64_t m = m0 + row, n = n0 + (row & 64) + strip_col(row & 63);
-      ra[e] = m < p.M ? *(const u32x4*)(p.a_codes + m * p.lda + kb * kKB + piece * 16) : u32x4{0u, 0u, 0u, 0u};
-      rb[e] = n < p.N ? *(const u32x4*)(p.b_codes + n * p.ldb + kb * kKB + piece * 16) : u32x4{0u, 0u, 0u, 0u};
-    }
-    float sa[4];
+  for (int j = 0; j < 4; ++j) rb[j] = read(sB[0] + wn * kKB, j);
+  fa[0] = read(sA[0] + wm * kKB, 0);
+  fa[1] = read(sA[0] + wm * kKB, 1);
+  read_sb(0);
+  for (int kt = 0; kt < nk; ++kt) {
+    Operand<kExact> fb[4], ax;
+    v4f d[4];
+    float s[4];
+    each<16>([&](auto index) {
+      constexpr int n = decltype(index)::value, i = n / 4, j = n % 4;
+      if constexpr (j == 0) {
+        if constexpr (i == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + wm + 16 * i + lrow;
-      sa[i] = m < p.M ? p.a_scales[kb * p.lda_scales + m] : 0.0f;
-    }
-    float sb[16];
-    if constexpr (KIND == MX_FP8_TILE) {
-      sb[0] = n0 < p.N ? p.b_scales[(n0 / kFp8Block) * p.ldb_scales + kb] : 0.0f;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sb[e] = col + e < p.N ? p.b_scales[kb * p.ldb_scales + col + e] : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = 32 * e + (t >> 3), piece = t & 7;
-      *(u32x4*)(sA + row * kKB + slot(row, piece)) = ra[e];
-      *(u32x4*)(sB + row * kKB + slot(row, piece)) = rb[e];
-    }
-    __syncthreads();
-    constexpr bool kExact = OUT == MX_OUT_F32;
-    Operand<kExact> fb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) fb[j] = operand<BF, kExact>(fragment(sB, wn + 16 * j + lrow, q));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const Operand<kExact> fa = operand<AF, kExact>(fragment(sA, wm + 16 * i + lrow, q));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const v4f d = mma<BF, AF, kExact>(fb[j], fa);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = fmaf(d[r], sa[i] * (KIND == MX_FP8_TILE ? sb[0] : sb[4 * j + r]), acc[i][j][r]);
+          for (int e = 0; e < 4; ++e) s[e] = sSA[st][wm + 16 * e + lrow];
+          fa[2] = read(sA[st] + wm * kKB, 2);
+        }
+        if constexpr (i == 1) fa[kRow3] = read(sA[st] + wm * kKB, 3);
+        if constexpr (i == 3) {
+          // every read of this stage is done, and the next one has landed
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          if (kt + 2 < nk) issue(st);
+          st ^= 1;
+        }
+        ax = operand<AF, kExact>(fa[i < 3 ? i : kRow3]);
+        if constexpr (i == 3) {
+          fa[0] = read(sA[st] + wm * kKB, 0);
+          fa[1] = read(sA[st] + wm * kKB, 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-  }
+      if constexpr (i == 0) fb[j] = operand<BF, kExact>(rb[j]);
+      if constexpr (n >= 4) {
+        if constexpr (KIND == MX_FP8_TILE && j == 0) s[i - 1] *= sb[0];
+        join(acc[i - 1][j], d[j], s[i - 1], j);
+      }
+      d[j] = mma<BF, AF, kExact>(fb[j], ax);
+      if constexpr (i == 3) rb[j] = read(sB[st] + wn * kKB, j);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (KIND == MX_FP8_TILE) s[3] *= sb[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) store_rows<OUT>(p, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
+    for (int j = 0; j < 4; ++j) join(acc[3][j], d[j], s[3], j);
+    read_sb(st);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (map.splits == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_rows<OUT>(p, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
+  } else {
+    Fp8GemmParams w = p;
+    w.c = map.parts + (int64_t)split * p.M * p.N;
+    w.ldc = p.N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_rows<MX_OUT_F32>(w, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
+  }
+}
+
+// C from the splits' sums, added in order; four columns a thread.
+template <int OUT>
+__global__ void __launch_bounds__(256) fp8_mm_sum(const Fp8GemmParams p, const float* parts, int splits) {
+  const int64_t quads = (p.N + 3) / 4, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= p.M * quads) return;
+  const int64_t m = at / quads, n = 4 * (at % quads);
+  const float* x = parts + m * p.N + n;
+  if (n + 4 <= p.N) {
+    v4f sum = *(const v4f_any*)x;
+    for (int i = 1; i < splits; ++i) sum += *(const v4f_any*)(x + i * p.M * p.N);
+    if constexpr (OUT == MX_OUT_F32) {
+      *(v4f_any*)((float*)p.c + m * p.ldc + n) = sum;
+    } else {
+      typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+      typedef u32x2 u32x2_any __attribute__((aligned(2)));
+      *(u32x2_any*)((uint16_t*)p.c + m * p.ldc + n) = u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+    }
+    return;
+  }
+  for (int r = 0; r < p.N - n; ++r) {
+    float sum = x[r];
+    for (int i = 1; i < splits; ++i) sum += x[i * p.M * p.N + r];
+    if constexpr (OUT == MX_OUT_F32) ((float*)p.c)[m * p.ldc + n + r] = sum;
+    else ((uint16_t*)p.c)[m * p.ldc + n + r] = (uint16_t)pack_bf16(sum, 0.0f);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -287,27 +531,8 @@ __global__ void __launch_bounds__(kGThreads) fp8_mm_any(const Fp8GemmParams p, i
 // Rows of a tile past the operand's last line read that line again (their
 // results are not stored), so every copy stays inside the operand and any M
 // and N run here.
-constexpr int kBT = 256, kBThreads = 512, kXcds = 8, kGroupM = 4, kGroupN = 8;
+constexpr int kBT = 256, kBThreads = 512, kGroupM = 4, kGroupN = 8;
 constexpr int kStage = kBT * kKB;
-
-// Global -> LDS copy of 16 (4) bytes per lane: LDS address = M0 + size * lane.  Inline asm, so that the
-// compiler places no waits of its own for it; it writes no register.  An SALU write of M0 needs one wait
-// state before the copy reads it.
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-template <typename T>
-__device__ __forceinline__ const T* uniform(const T* p) {
-  const uint64_t v = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const T*)(((uint64_t)hi << 32) | lo);
-}
 
 // Tiles are dealt in groups of 4 (M) x 8 (N) to the 8 XCDs, a group to the 32 CUs of one, so that the tiles
 // an XCD computes at once share 4 A strips and 8 B strips in its L2.
@@ -548,16 +773,56 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
   }
 }
 
-// The large-product kernel's copies address a tile's rows by 32-bit offsets whose row pitch is a 24-bit factor.
-bool big_offsets(const Fp8GemmParams& p) {
+// How a product runs.  The copies of the two tiled kernels address a tile's rows by 32-bit offsets whose row pitch
+// is a 24-bit factor; operands with longer rows run on the kernel for few rows, 64 rows of A at a time.
+enum class Path { kFew, kMid, kBig };
+
+struct Plan {
+  Path path;
+  int splits;
+};
+
+Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lda_scales, int64_t ldb_scales,
+             int out_kind) {
   const int64_t lim = int64_t(1) << 24;
-  return p.lda < lim && p.ldb < lim && p.lda_scales < lim && p.ldb_scales < lim && p.K < (int64_t(1) << 30);
+  if (M <= 64 || lda >= lim || ldb >= lim || lda_scales >= lim || ldb_scales >= lim) return {Path::kFew, 1};
+  const int64_t nk = (K + kKB - 1) / kKB;
+  const int64_t big = ((M + kBT - 1) / kBT) * ((N + kBT - 1) / kBT);
+  if (out_kind == MX_OUT_BF16 && big >= 192) return {Path::kBig, 1};
+  const int64_t tiles = ((M + kMT - 1) / kMT) * ((N + kMT - 1) / kMT);
+  int64_t splits = 1;
+  while (tiles * splits * 2 <= 512 && nk >= 8 * splits * 2) splits *= 2;
+  return {Path::kMid, (int)splits};
+}
+
+template <int AF, int BF, int KIND, int OUT, int F>
+void launch_few(const Fp8GemmParams& p, hipStream_t s) {
+  for (int64_t m = 0; m < p.M; m += 64) {
+    Fp8GemmParams r = p;
+    r.a_codes += m * p.lda;
+    r.a_scales += m;
+    r.M = p.M - m < 64 ? p.M - m : 64;
+    r.c = (uint8_t*)p.c + m * p.ldc * (OUT == MX_OUT_F32 ? 4 : 2);
+    if (p.N >= 32 * 256)
+      hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, 2>), dim3((unsigned)((p.N + 31) / 32)),
+                         dim3(64 * kFewWaves), 0, s, r);
+    else
+      hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, 1>), dim3((unsigned)((p.N + 15) / 16)),
+                         dim3(64 * kFewWaves), 0, s, r);
+  }
 }
 
 template <int AF, int BF, int KIND, int OUT>
-void launch(const Fp8GemmParams& p, hipStream_t s) {
+void launch(const Fp8GemmParams& p, float* parts, int64_t parts_bytes, hipStream_t s) {
+  Plan plan = plan_of(p.M, p.N, p.K, p.lda, p.ldb, p.lda_scales, p.ldb_scales, OUT);
+  if (plan.path == Path::kFew) {
+    if (p.M <= 16) launch_few<AF, BF, KIND, OUT, 1>(p, s);
+    else if (p.M <= 32) launch_few<AF, BF, KIND, OUT, 2>(p, s);
+    else launch_few<AF, BF, KIND, OUT, 4>(p, s);
+    return;
+  }
   if constexpr (OUT == MX_OUT_BF16) {
-    if (p.M >= kBT && p.N >= kBT && big_offsets(p)) {
+    if (plan.path == Path::kBig) {
       BigMap map;
       map.tiles_m = (int)((p.M + kBT - 1) / kBT);
       map.tiles_n = (int)((p.N + kBT - 1) / kBT);
@@ -568,28 +833,50 @@ void launch(const Fp8GemmParams& p, hipStream_t s) {
       return;
     }
   }
-  const int64_t tm = (p.M + kGT - 1) / kGT, tn = (p.N + kGT - 1) / kGT;
-  hipLaunchKernelGGL((fp8_mm_any<AF, BF, KIND, OUT>), dim3((unsigned)(tm * tn)), dim3(kGThreads), 0, s, p, tm);
+  // the workspace holds as many sums as it can
+  while (plan.splits > 1 && (parts == nullptr || parts_bytes / 4 / plan.splits / p.M < p.N)) --plan.splits;
+  MidMap map;
+  map.tiles_m = (int)((p.M + kMT - 1) / kMT);
+  map.tiles_n = (int)((p.N + kMT - 1) / kMT);
+  map.splits = plan.splits;
+  map.total = map.tiles_m * map.tiles_n * map.splits;
+  map.per_xcd = (map.total + kXcds - 1) / kXcds;
+  map.parts = parts;
+  hipLaunchKernelGGL((fp8_mm_mid<AF, BF, KIND, OUT>), dim3((unsigned)(kXcds * map.per_xcd)), dim3(kMThreads), 0, s, p,
+                     map);
+  if (map.splits > 1) {
+    const int64_t quads = p.M * ((p.N + 3) / 4);
+    hipLaunchKernelGGL((fp8_mm_sum<OUT>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, p, parts,
+                       map.splits);
+  }
 }
 
 template <int AF, int BF>
-void launch_kinds(const Fp8GemmParams& p, int b_kind, int out_kind, hipStream_t s) {
+void launch_kinds(const Fp8GemmParams& p, int b_kind, int out_kind, float* w, int64_t bytes, hipStream_t s) {
   if (b_kind == MX_FP8_TILE) {
-    if (out_kind == MX_OUT_F32) launch<AF, BF, MX_FP8_TILE, MX_OUT_F32>(p, s);
-    else launch<AF, BF, MX_FP8_TILE, MX_OUT_BF16>(p, s);
+    if (out_kind == MX_OUT_F32) launch<AF, BF, MX_FP8_TILE, MX_OUT_F32>(p, w, bytes, s);
+    else launch<AF, BF, MX_FP8_TILE, MX_OUT_BF16>(p, w, bytes, s);
   } else {
-    if (out_kind == MX_OUT_F32) launch<AF, BF, MX_FP8_LINE, MX_OUT_F32>(p, s);
-    else launch<AF, BF, MX_FP8_LINE, MX_OUT_BF16>(p, s);
+    if (out_kind == MX_OUT_F32) launch<AF, BF, MX_FP8_LINE, MX_OUT_F32>(p, w, bytes, s);
+    else launch<AF, BF, MX_FP8_LINE, MX_OUT_BF16>(p, w, bytes, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8GemmParams& p, int a_fmt, int b_fmt, int b_kind, int out_kind, hipStream_t s) {
-  if (a_fmt == MX_FP8_E4M3 && b_fmt == MX_FP8_E4M3) launch_kinds<MX_FP8_E4M3, MX_FP8_E4M3>(p, b_kind, out_kind, s);
-  else if (a_fmt == MX_FP8_E5M2 && b_fmt == MX_FP8_E4M3) launch_kinds<MX_FP8_E5M2, MX_FP8_E4M3>(p, b_kind, out_kind, s);
-  else if (a_fmt == MX_FP8_E4M3) launch_kinds<MX_FP8_E4M3, MX_FP8_E5M2>(p, b_kind, out_kind, s);
-  else launch_kinds<MX_FP8_E5M2, MX_FP8_E5M2>(p, b_kind, out_kind, s);
+int64_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, int out_kind) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  const int64_t k = ((K + kKB - 1) / kKB) * kKB;
+  const Plan plan = plan_of(M, N, K, k, k, 1, 1, out_kind);
+  return plan.splits > 1 ? 4 * plan.splits * M * N : 0;
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmParams& p, int a_fmt, int b_fmt, int b_kind, int out_kind, float* parts,
+                           int64_t bytes, hipStream_t s) {
+  if (a_fmt == MX_FP8_E4M3 && b_fmt == MX_FP8_E4M3) launch_kinds<MX_FP8_E4M3, MX_FP8_E4M3>(p, b_kind, out_kind, parts, bytes, s);
+  else if (a_fmt == MX_FP8_E5M2 && b_fmt == MX_FP8_E4M3) launch_kinds<MX_FP8_E5M2, MX_FP8_E4M3>(p, b_kind, out_kind, parts, bytes, s);
+  else if (a_fmt == MX_FP8_E4M3) launch_kinds<MX_FP8_E4M3, MX_FP8_E5M2>(p, b_kind, out_kind, parts, bytes, s);
+  else launch_kinds<MX_FP8_E5M2, MX_FP8_E5M2>(p, b_kind, out_kind, parts, bytes, s);
   return hipGetLastError();
 }
 

@@ -37,7 +37,10 @@ struct Fp8GemmParams {
   int64_t ldc;
 };
 
-hipError_t launch_fp8_gemm(const Fp8GemmParams& p, int a_fmt, int b_fmt, int b_kind, int out_kind, hipStream_t s);
+// parts: float32 workspace of `bytes` bytes (may be null)
+hipError_t launch_fp8_gemm(const Fp8GemmParams& p, int a_fmt, int b_fmt, int b_kind, int out_kind, float* parts,
+                           int64_t bytes, hipStream_t s);
+int64_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, int out_kind);
 
 // One AdamW step.  Up to kAdamwGroup tensors ride in one launch's arguments.
 constexpr int kAdamwGroup = 48;

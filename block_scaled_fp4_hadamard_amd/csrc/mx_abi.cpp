@@ -461,7 +461,7 @@ mx_status mx_fp8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t
 
 mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_tensor* b, mx_fp8_fmt b_fmt,
                       mx_fp8_kind b_kind, int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, mx_out out,
-                      void* hip_stream) {
+                      void* workspace, int64_t workspace_bytes, void* hip_stream) {
   if (M < 0 || N < 0 || K <= 0) return MX_ERR_INVALID;
   if (!fp8_fmt_ok(a_fmt) || !fp8_fmt_ok(b_fmt) || !fp8_kind_ok(b_kind)) return MX_ERR_INVALID;
   if (out != MX_OUT_F32 && out != MX_OUT_BF16) return MX_ERR_INVALID;
@@ -472,6 +472,7 @@ mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_ten
   if (s != MX_OK) return s;
   const uintptr_t esize = out == MX_OUT_F32 ? 4u : 2u;
   if (c == nullptr || ((uintptr_t)c % esize) != 0 || ldc < N || too_many_tiles(M, N)) return MX_ERR_INVALID;
+  if (workspace_bytes < 0 || !aligned16(workspace)) return MX_ERR_INVALID;
   mx::Fp8GemmParams p{};
   p.a_codes = a->codes;
   p.b_codes = b->codes;
@@ -486,8 +487,14 @@ mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_ten
   p.K = K;
   p.c = c;
   p.ldc = ldc;
-  const hipError_t e = mx::launch_fp8_gemm(p, a_fmt, b_fmt, b_kind, out, (hipStream_t)hip_stream);
+  const hipError_t e = mx::launch_fp8_gemm(p, a_fmt, b_fmt, b_kind, out, (float*)workspace, workspace_bytes,
+                                             (hipStream_t)hip_stream);
   return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out) {
+  if (out != MX_OUT_F32 && out != MX_OUT_BF16) return 0;
+  return mx::fp8_gemm_workspace(M, N, K, out);
 }
 
 mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t bits, const mx_adamw_params* params,

@@ -149,8 +149,9 @@ def test_quantize_validation(kw, want):
     assert quant(**kw) == want
 
 
-def gemm(a="d", af=0, b="d", bf=0, kind=0, M=64, N=64, K=128, c=FAKE, ldc=64, out=0):
-    return _lib.mx_fp8_gemm(f8() if a == "d" else a, af, f8() if b == "d" else b, bf, kind, M, N, K, c, ldc, out, None)
+def gemm(a="d", af=0, b="d", bf=0, kind=0, M=64, N=64, K=128, c=FAKE, ldc=64, out=0, ws=None, wsb=0):
+    return _lib.mx_fp8_gemm(f8() if a == "d" else a, af, f8() if b == "d" else b, bf, kind, M, N, K, c, ldc, out,
+                            ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -158,7 +159,7 @@ def gemm(a="d", af=0, b="d", bf=0, kind=0, M=64, N=64, K=128, c=FAKE, ldc=64, ou
     (dict(kind=2), 1), (dict(out=2), 1), (dict(a=f8(ld=64)), 1), (dict(K=129), 1), (dict(a=f8(lds=63)), 1),
     (dict(b=f8(lds=63)), 1), (dict(kind=1, b=f8(lds=0)), 1), (dict(a=f8(codes=0)), 1), (dict(b=f8(scales=0)), 1),
     (dict(b=f8(codes=FAKE + 4)), 1), (dict(c=0), 1), (dict(c=FAKE + 2), 1), (dict(c=FAKE + 1, out=1), 1),
-    (dict(ldc=63), 1), (dict(M=0), 0), (dict(N=0), 0),
+    (dict(ldc=63), 1), (dict(ws=FAKE + 8, wsb=64), 1), (dict(wsb=-1), 1), (dict(M=0), 0), (dict(N=0), 0),
 ])
 def test_gemm_validation(kw, want):
     assert gemm(**kw) == want

@@ -141,23 +141,53 @@ typedef v4f v4f_any __attribute__((aligned(4)));
 // A wave's 16 rows x 64 columns of C from its accumulators: row m0 + l % 16, columns n0 + 16 (l / 16) .. + 15 in
 // lane l.  Non-temporal: the output streams past the L2, which keeps the operand rows that the next tiles read.
 // bf16: lanes l and l ^ 8 trade halves of their 32 bytes, so that each store writes whole 128-byte pieces of
-// eight rows.  The last columns of an odd width go one by one.
-template <int OUT>
+// eight rows.  fp32: each quad of lanes transposes its 4 x 4 pieces of 16 bytes, so that each store writes
+// whole 256-byte pieces of four rows (a lane's own 64 bytes, stored as they are, reached 0.9 TB/s).  The last
+// columns of an odd width go one by one.  KEEP: sums that are read again soon stay in the caches.
+__device__ __forceinline__ float dpp_xor1(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
+}
+__device__ __forceinline__ float dpp_xor2(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
+}
+
+template <int OUT, bool KEEP = false>
 __device__ __forceinline__ void store_rows(const Fp8GemmParams& p, int64_t m0, int64_t n0, int lane,
                                            const v4f (&acc)[4]) {
   const int lrow = lane & 15, q = lane >> 4;
   if constexpr (OUT == MX_OUT_F32) {
-    const int64_t m = m0 + lrow, n = n0 + 16 * q;
-    if (m >= p.M) return;
-    float* c = (float*)p.c + m * p.ldc + n;
+    // t[e] of lane 4 y + x: row 4 y + x, piece e; transposed, row 4 y + e, piece x
+    v4f t[4] = {acc[0], acc[1], acc[2], acc[3]};
+    const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + 4 * j + 4 <= p.N) {
-        __builtin_nontemporal_store(acc[j], (v4f_any*)(c + 4 * j));
+    for (int r = 0; r < 4; r += 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float got = dpp_xor1(odd ? t[r][e] : t[r + 1][e]);
+        t[r][e] = odd ? got : t[r][e];
+        t[r + 1][e] = odd ? t[r + 1][e] : got;
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float got = dpp_xor2(high ? t[r][e] : t[r + 2][e]);
+        t[r][e] = high ? got : t[r][e];
+        t[r + 2][e] = high ? t[r + 2][e] : got;
+      }
+    const int64_t n = n0 + 16 * q + 4 * (lrow & 3);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t m = m0 + (lrow & 12) + e;
+      if (m >= p.M) continue;
+      float* c = (float*)p.c + m * p.ldc + n;
+      if (n + 4 <= p.N) {
+        if constexpr (KEEP) *(v4f_any*)c = t[e];
+        else __builtin_nontemporal_store(t[e], (v4f_any*)c);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (n + 4 * j + r < p.N) c[4 * j + r] = acc[j][r];
+          if (n + r < p.N) c[r] = t[e][r];
       }
     }
   } else {
@@ -479,7 +509,7 @@ __global__ void __launch_bounds__(kMThreads, 2) fp8_mm_mid(const Fp8GemmParams p
     w.c = map.parts + (int64_t)split * p.M * p.N;
     w.ldc = p.N;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store_rows<MX_OUT_F32>(w, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
+    for (int i = 0; i < 4; ++i) store_rows<MX_OUT_F32, true>(w, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
   }
 }
 

@@ -2,7 +2,6 @@
 the tensor's device and launch on torch's current stream.  No arithmetic of
 the method happens here.
 """
-import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -317,22 +316,30 @@ def _fp8_blocks(n):
     return -(-n // FP8_BLOCK)
 
 
-def _pitch(t, name):
-    """Elements between the rows of a 2-D tensor with unit column stride whose rows do not overlap."""
-    if t.shape[1] > 1 and t.stride(1) != 1:
+_OUT_KINDS = {torch.float32: _lib.OUT["f32"], torch.bfloat16: _lib.OUT["bf16"]}
+
+
+def _pitch(stride, rows, cols, name):
+    """Elements between the rows of a rows x cols tensor of this stride: unit column stride, rows that do not overlap."""
+    ld, one = stride
+    if cols > 1 and one != 1:
         raise ValueError("%s must have unit column stride" % name)
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError("%s: its rows overlap (a stride of %d for %d columns)" % (name, t.stride(0), t.shape[1]))
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if rows > 1 and ld < cols:
+        raise ValueError("%s: its rows overlap (a stride of %d for %d columns)" % (name, ld, cols))
+    return ld if rows > 1 else cols
 
 
-def _launch_on(dev):
-    """Refuses host tensors, and makes dev the current device for a launch on its stream."""
+def _launch(dev, name, entry, *args):
+    """entry(*args, stream) on dev's current stream, with dev the current device; host tensors are refused."""
     if dev.type != "cuda":
         raise ValueError("the operands must be CUDA tensors, got %s" % dev)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index) or None
+    if dev.index == torch.cuda.current_device():
+        st = entry(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = entry(*args, stream)
+    _lib.check(st, name)
 
 
 @dataclass
@@ -354,23 +361,25 @@ class Fp8Tensor:
         return self.codes.shape[0]
 
     def check(self, name):
+        """The operand as the library takes it; ValueError if its tensors are not what the class describes."""
+        codes, scales = self.codes, self.scales
         if self.fmt not in _lib.FP8_FMT or self.kind not in _lib.FP8_KIND:
             raise ValueError("%s: unknown format %r or kind %r" % (name, self.fmt, self.kind))
         kb = _fp8_blocks(self.k)
-        if self.codes.dtype != torch.uint8 or self.codes.dim() != 2 or self.codes.shape[1] != kb * FP8_BLOCK:
+        shape, sshape = codes.shape, scales.shape
+        if codes.dtype != torch.uint8 or len(shape) != 2 or shape[1] != kb * FP8_BLOCK:
             raise ValueError("%s: codes must be uint8 (lines, %d) for k = %d" % (name, kb * FP8_BLOCK, self.k))
-        lines = self.codes.shape[0]
-        shape = (kb, lines) if self.kind == "line" else (_fp8_blocks(lines), kb)
-        if self.scales.dtype != torch.float32 or tuple(self.scales.shape) != shape:
-            raise ValueError("%s: scales must be float32 %s for kind %r" % (name, shape, self.kind))
-        _pitch(self.codes, name + ".codes")
-        _pitch(self.scales, name + ".scales")
-        if self.scales.device != self.codes.device:
+        lines, width = shape
+        rows, cols = (kb, lines) if self.kind == "line" else (_fp8_blocks(lines), kb)
+        if scales.dtype != torch.float32 or len(sshape) != 2 or sshape[0] != rows or sshape[1] != cols:
+            raise ValueError("%s: scales must be float32 %s for kind %r" % (name, (rows, cols), self.kind))
+        if scales.device != codes.device:
             raise ValueError("%s: codes and scales are on different devices" % name)
+        return _lib.Fp8TensorC(codes.data_ptr(), _pitch(codes.stride(), lines, width, name),
+                               scales.data_ptr(), _pitch(scales.stride(), rows, cols, name))
 
     def c_struct(self):
-        return _lib.fp8_tensor(self.codes.data_ptr(), _pitch(self.codes, "codes"),
-                               self.scales.data_ptr(), _pitch(self.scales, "scales"))
+        return self.check("operand")
 
 
 def empty_fp8(lines, k, device, fmt="e4m3", kind="line"):
@@ -389,66 +398,60 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
     """
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
+    if x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError("x must be bfloat16 (or its 16-bit patterns), got %s" % x.dtype)
     if axis not in _lib.AXIS or kind not in _lib.FP8_KIND or fmt not in _lib.FP8_FMT:
         raise ValueError("unknown axis %r, kind %r or format %r" % (axis, kind, fmt))
-    xb = _bits_view(x)
     rows, cols = x.shape
+    ld = _pitch(x.stride(), rows, cols, "x")
     dev = x.device
     out = {}
-    rq = cq = None
-    for name, given, lines, k in (("row", row_out, rows, cols), ("col", col_out, cols, rows)):
-        if axis not in (name, "both"):
+    c = [None, None]
+    for i, (name, given, lines, k) in enumerate((("row", row_out, rows, cols), ("col", col_out, cols, rows))):
+        if axis != name and axis != "both":
             continue
         q = given
         if q is None:
             q = empty_fp8(lines, k, dev, fmt, kind)
-        else:
-            q.check(name + "_out")
-            if (q.lines, q.k, q.fmt, q.kind) != (lines, k, fmt, kind) or q.codes.device != dev:
-                raise ValueError("%s_out is not an %s operand of %d %s lines of %d values on %s"
-                                 % (name, fmt, lines, kind, k, dev))
+        elif (q.lines, q.k, q.fmt, q.kind) != (lines, k, fmt, kind) or q.codes.device != dev:
+            raise ValueError("%s_out is not an %s operand of %d %s lines of %d values on %s"
+                             % (name, fmt, lines, kind, k, dev))
         out[name] = q
-        if name == "row":
-            rq = q.c_struct()
-        else:
-            cq = q.c_struct()
-    with _launch_on(dev):
-        st = _lib.mx_fp8_quantize(xb.data_ptr(), rows, cols, _pitch(x, "x"),
-                                  _lib.FP8_FMT[fmt], _lib.FP8_KIND[kind], _lib.AXIS[axis], rq, cq, _stream(dev))
-    _lib.check(st, "mx_fp8_quantize")
+        c[i] = q.check(name + "_out")
+    _launch(dev, "mx_fp8_quantize", _lib.mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _lib.FP8_FMT[fmt],
+            _lib.FP8_KIND[kind], _lib.AXIS[axis], *c)
     return out
 
 
 def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
     """C = A B^T (M x N) on two 8-bit operands' values, fp32 accumulation, fp32 or bf16 output.
 
-    a is scaled by lines (kind "line"), b by lines or tiles; each may be E4M3 or E5M2.
+    a is scaled by lines (kind "line"), b by lines or tiles; each may be E4M3 or E5M2.  bf16 output runs on the 8-bit
+    matrix instruction; fp32 output on the bf16 one, whose products are exact, at half its rate.
     """
-    a.check("a")
-    b.check("b")
+    ca, cb = a.check("a"), b.check("b")
     if a.k != b.k:
         raise ValueError("operands disagree on K: %d vs %d" % (a.k, b.k))
     if a.kind != "line":
         raise ValueError("a must be scaled by lines, got kind %r" % a.kind)
     dev = a.codes.device
-    M, N = a.lines, b.lines
+    M, N = a.codes.shape[0], b.codes.shape[0]
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     elif out.dim() != 2 or out.shape[0] != M or out.shape[1] != N:
         raise ValueError("out must be a row-major (%d, %d) view" % (M, N))
-    if out.dtype not in (torch.float32, torch.bfloat16):
+    kind = _OUT_KINDS.get(out.dtype)
+    if kind is None:
         raise ValueError("the output must be float32 or bfloat16, got %s" % out.dtype)
     if b.codes.device != dev or out.device != dev:
         raise ValueError("a, b and out must be on one device")
-    kind = _lib.OUT["f32" if out.dtype == torch.float32 else "bf16"]
-    with _launch_on(dev):
-        # the workspace is this call's own: the allocator gives its memory to later work of the same stream only
-        size = _lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
-        space = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-        st = _lib.mx_fp8_gemm(a.c_struct(), _lib.FP8_FMT[a.fmt], b.c_struct(), _lib.FP8_FMT[b.fmt],
-                              _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), _pitch(out, "out"), kind,
-                              space.data_ptr() if size else None, size, _stream(dev))
-    _lib.check(st, "mx_fp8_gemm")
+    ldc = _pitch(out.stride(), M, N, "out")
+    # the workspace is this call's own: held until the launch, its memory then goes to later work of this stream only
+    size = _lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
+    space = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _launch(dev, "mx_fp8_gemm", _lib.mx_fp8_gemm, ca, _lib.FP8_FMT[a.fmt], cb, _lib.FP8_FMT[b.fmt],
+            _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), ldc, kind,
+            space.data_ptr() if size else None, size)
     return out
 
 
@@ -569,7 +572,8 @@ def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
             raise ValueError("grad_scale must be a one-element torch.float32 tensor on %s" % dev)
         _, scale = _scalar(grad_scale, torch.float32, "grad_scale", dev)
     params = _lib.AdamwParamsC(lr, beta1, beta2, eps, weight_decay, step, step_dev, lr_dev, scale)
-    with _launch_on(dev) if dev is not None else contextlib.nullcontext():
-        st = _lib.mx_adamw_step(tensors._c, len(tensors.params), tensors.bits, params, _lib.ROUND[rounding], seed,
-                                _stream(dev) if dev is not None else None)
-    _lib.check(st, "mx_adamw_step")
+    args = (tensors._c, len(tensors.params), tensors.bits, params, _lib.ROUND[rounding], seed)
+    if dev is None:
+        _lib.check(_lib.mx_adamw_step(*args, None), "mx_adamw_step")       # an empty list: only the checks run
+    else:
+        _launch(dev, "mx_adamw_step", _lib.mx_adamw_step, *args)

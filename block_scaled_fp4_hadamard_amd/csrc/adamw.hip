@@ -23,7 +23,7 @@
 // 8-bit ones.  A lane takes eight consecutive elements, so that 16 lanes (a
 // DPP row) hold a block of 128 and its maximum needs no LDS.  The tensors'
 // addresses ride in the kernel's arguments, 48 to a launch, so a step needs no
-// table in device memory; a persistent grid walks 2048-element chunks.
+// table in device memory; a workgroup takes 4096 elements.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -37,9 +37,9 @@ namespace mx {
 
 namespace {
 
-constexpr int kAwThreads = 256;
+constexpr int kAwThreads = 512;
 constexpr int kAwChunk = 8 * kAwThreads;
-constexpr unsigned kAwGrid = 2048;         // 8 workgroups on each of the 256 CUs
+constexpr unsigned kAwGrid = 1024;         // 4 workgroups on each of the 256 CUs
 
 struct AdamwArgs {
   AdamwTensor t[kAdamwGroup];
@@ -295,7 +295,10 @@ hipError_t launch_adamw(const AdamwTensor* tensors, const bool* grad_bf16, int c
     a.flags[i] = (uint8_t)((bf ? 1 : 0) | (vectors(a.t[i], bf, bits) ? 2 : 0));
   }
   if (chunks == 0) return hipSuccess;
-  const dim3 g(chunks < kAwGrid ? chunks : kAwGrid), b(kAwThreads);
+  // one workgroup a chunk (5.4 TB/s on a block's weights against 5.0 with a resident grid); where each workgroup forms
+  // the coefficients itself, a resident grid, so that the few thousand instructions of it are paid once
+  const bool form = step.step_dev != nullptr || step.lr_dev != nullptr;
+  const dim3 g(form && chunks > kAwGrid ? kAwGrid : chunks), b(kAwThreads);
   if (bits == 32) hipLaunchKernelGGL((adamw_kernel<32, MX_ROUND_RTNE>), g, b, 0, s, a);
   else if (round == MX_ROUND_SR) hipLaunchKernelGGL((adamw_kernel<8, MX_ROUND_SR>), g, b, 0, s, a);
   else hipLaunchKernelGGL((adamw_kernel<8, MX_ROUND_RTNE>), g, b, 0, s, a);

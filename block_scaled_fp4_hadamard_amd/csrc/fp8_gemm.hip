@@ -71,62 +71,43 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
-// An operand fragment as the matrix instruction of the output type takes it.
-template <bool EXACT>
-struct Operand;
-
-template <>
-struct Operand<false> {
-  v8i x;
-};
-
-template <>
-struct Operand<true> {
-  bf16x8_t x[4];       // bytes 8 q .. 8 q + 7 of the lane's 32
-};
-
-// eight codes of one format as bf16
+// Two codes (the low or the high half of a dword) as packed bf16, exact.
 template <int FMT>
-__device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi) {
-  bf16x2_t v[4];
-  if constexpr (FMT == MX_FP8_E4M3) {
-    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  } else {
-    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
-  }
-  return bf16x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+__device__ __forceinline__ uint32_t widen(uint32_t codes, bool high) {
+  if constexpr (FMT == MX_FP8_E4M3)
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, false));
+  else
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, false));
 }
 
-template <int FMT, bool EXACT>
-__device__ __forceinline__ Operand<EXACT> operand(const v8i& x) {
-  Operand<EXACT> o;
-  if constexpr (EXACT) {
+// A fragment's 32 codes of a lane as bf16, eight for each of four 32-deep instructions.
+struct Wide {
+  uint32_t w[16];
+};
+
+template <int FMT>
+__device__ __forceinline__ Wide widen(const v8i& x) {
+  Wide o;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) o.x[q] = widen<FMT>((uint32_t)x[2 * q], (uint32_t)x[2 * q + 1]);
-  } else {
-    o.x = x;
-  }
+  for (int c = 0; c < 16; ++c) o.w[c] = widen<FMT>((uint32_t)x[c >> 1], (c & 1) != 0);
   return o;
+}
+
+// codes 8 q .. 8 q + 7 of one block's product
+__device__ __forceinline__ v4f mma_wide(const Wide& b, const Wide& a, int q, const v4f& d) {
+  const u32x4 x = {b.w[4 * q], b.w[4 * q + 1], b.w[4 * q + 2], b.w[4 * q + 3]};
+  const u32x4 y = {a.w[4 * q], a.w[4 * q + 1], a.w[4 * q + 2], a.w[4 * q + 3]};
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, y), d, 0,
+                                                 0, 0);
 }
 
 // One block's product of two fragments.  Format codes: 0 E4M3, 1 E5M2; zero scale operands select the
 // instruction without block scales.
-template <int BF, int AF, bool EXACT>
-__device__ __forceinline__ v4f mma(const Operand<EXACT>& b, const Operand<EXACT>& a) {
-  v4f d = v4f{0.f, 0.f, 0.f, 0.f};
-  if constexpr (EXACT) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.x[q], a.x[q], d, 0, 0, 0);
-  } else {
-    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.x, a.x, d, BF, AF, 0, 0, 0, 0);
-  }
-  return d;
+template <int BF, int AF>
+__device__ __forceinline__ v4f mma(const v8i& b, const v8i& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, v4f{0.f, 0.f, 0.f, 0.f}, BF, AF, 0, 0, 0, 0);
 }
 
 // round to nearest even, NaN quieted
@@ -312,15 +293,24 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool counts = kb + u * kFewWaves < nk;
-      Operand<kExact> ob[J];
+      Wide ob[J];
+      if constexpr (kExact) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) ob[j] = operand<BF, kExact>(rb[u][j]);
+        for (int j = 0; j < J; ++j) ob[j] = widen<BF>(rb[u][j]);
+      }
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const Operand<kExact> oa = operand<AF, kExact>(ra[u][f]);
+        Wide oa;
+        if constexpr (kExact) oa = widen<AF>(ra[u][f]);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          const v4f d = mma<BF, AF, kExact>(ob[j], oa);
+          v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+          if constexpr (kExact) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d = mma_wide(ob[j], oa, e, d);
+          } else {
+            d = mma<BF, AF>(rb[u][j], ra[u][f]);
+          }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float s = ca[u][f] * cb[u][j][KIND == MX_FP8_TILE ? 0 : r];
@@ -451,55 +441,127 @@ __global__ void __launch_bounds__(kMThreads, 2) fp8_mm_mid(const Fp8GemmParams p
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
   if (nk > 1) issue(1);
   int st = 0;
-  // A fragment row i in fa[i], B fragments as read; the widened form leaves no registers for row 3's own place,
-  // which row 0, widened by then, gives up
-  constexpr int kRow3 = kExact ? 0 : 3;
-  v8i fa[kExact ? 3 : 4], rb[4];
+  auto row = [&](int i) { return read(sA[st] + wm * kKB, i); };
+  auto column = [&](int j) { return read(sB[st] + wn * kKB, j); };
+  auto next_stage = [&](int kt) {
+    // every read of this stage is done, and the next one has landed
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + 2 < nk) issue(st);
+    st ^= 1;
+  };
+  if constexpr (!kExact) {
+    v8i fa[4], fb[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) rb[j] = read(sB[0] + wn * kKB, j);
-  fa[0] = read(sA[0] + wm * kKB, 0);
-  fa[1] = read(sA[0] + wm * kKB, 1);
-  read_sb(0);
-  for (int kt = 0; kt < nk; ++kt) {
-    Operand<kExact> fb[4], ax;
-    v4f d[4];
-    float s[4];
-    each<16>([&](auto index) {
-      constexpr int n = decltype(index)::value, i = n / 4, j = n % 4;
-      if constexpr (j == 0) {
-        if constexpr (i == 0) {
+    for (int j = 0; j < 4; ++j) fb[j] = column(j);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[e] = sSA[st][wm + 16 * e + lrow];
-          fa[2] = read(sA[st] + wm * kKB, 2);
+    for (int i = 0; i < 2; ++i) fa[i] = row(i);
+    read_sb(0);
+    for (int kt = 0; kt < nk; ++kt) {
+      v4f d[4];
+      float s[4];
+      each<16>([&](auto index) {
+        constexpr int n = decltype(index)::value, i = n / 4, j = n % 4;
+        if constexpr (j == 0) {
+          if constexpr (i == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = sSA[st][wm + 16 * e + lrow];
+          }
+          if constexpr (i < 2) fa[i + 2] = row(i + 2);
+          if constexpr (i == 3) {
+            next_stage(kt);
+            fa[0] = row(0);
+            fa[1] = row(1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (i == 1) fa[kRow3] = read(sA[st] + wm * kKB, 3);
-        if constexpr (i == 3) {
-          // every read of this stage is done, and the next one has landed
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          if (kt + 2 < nk) issue(st);
-          st ^= 1;
+        if constexpr (n >= 4) {
+          if constexpr (KIND == MX_FP8_TILE && j == 0) s[i - 1] *= sb[0];
+          join(acc[i - 1][j], d[j], s[i - 1], j);
         }
-        ax = operand<AF, kExact>(fa[i < 3 ? i : kRow3]);
-        if constexpr (i == 3) {
-          fa[0] = read(sA[st] + wm * kKB, 0);
-          fa[1] = read(sA[st] + wm * kKB, 1);
-        }
+        d[j] = mma<BF, AF>(fb[j], fa[i]);
+        if constexpr (i == 3) fb[j] = column(j);
         __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (i == 0) fb[j] = operand<BF, kExact>(rb[j]);
-      if constexpr (n >= 4) {
-        if constexpr (KIND == MX_FP8_TILE && j == 0) s[i - 1] *= sb[0];
-        join(acc[i - 1][j], d[j], s[i - 1], j);
-      }
-      d[j] = mma<BF, AF, kExact>(fb[j], ax);
-      if constexpr (i == 3) rb[j] = read(sB[st] + wn * kKB, j);
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    if constexpr (KIND == MX_FP8_TILE) s[3] *= sb[0];
+      });
+      if constexpr (KIND == MX_FP8_TILE) s[3] *= sb[0];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) join(acc[3][j], d[j], s[3], j);
-    read_sb(st);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < 4; ++j) join(acc[3][j], d[j], s[3], j);
+      read_sb(st);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    // Product n of a step is four 32-deep instructions, and beside each of them run one element of an earlier
+    // product's join and one widening of the next A fragment (two in row 3, whose next fragment has just been asked
+    // for).  The next step's B fragments are widened as this step's are done with, at products 14, 15, 0 and 1.
+    v8i fa[2], rb[2];                        // as read: A row i in fa[i % 2], B column j in rb[j % 2]
+    Wide ax, an, fb[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb[j] = widen<BF>(column(j));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) rb[j] = column(2 + j);
+    ax = widen<AF>(row(0));
+    fa[1] = row(1);
+    read_sb(0);
+    for (int kt = 0; kt < nk; ++kt) {
+      v4f d[4];
+      float s[4];
+      each<16>([&](auto index) {
+        constexpr int n = decltype(index)::value, i = n / 4, j = n % 4;
+        if constexpr (j == 0) {
+          if constexpr (i == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = sSA[st][wm + 16 * e + lrow];
+          }
+          if constexpr (i < 2) fa[i & 1] = row(i + 2);
+          if constexpr (i == 3) {
+            next_stage(kt);
+            fa[0] = row(0);
+            rb[0] = column(0);
+            rb[1] = column(1);
+            fa[1] = row(1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        constexpr int m = n - 3, mi = m / 4, mj = m & 3;
+        if constexpr (m >= 0 && KIND == MX_FP8_TILE && mj == 0) s[mi] *= sb[0];
+        constexpr int bj = n == 14 ? 0 : n == 15 ? 1 : n == 0 ? 2 : n == 1 ? 3 : -1;
+        v4f x = v4f{0.f, 0.f, 0.f, 0.f};
+        each<4>([&](auto part) {
+          constexpr int e = decltype(part)::value;
+          x = mma_wide(fb[j], ax, e, x);
+          if constexpr (m >= 0) {
+            acc[mi][mj][e] = fmaf(d[mj][e], KIND == MX_FP8_LINE ? s[mi] * sb[4 * mj + e] : s[mi], acc[mi][mj][e]);
+          }
+          if constexpr (i < 3) {
+            constexpr int c = 4 * j + e;
+            an.w[c] = widen<AF>((uint32_t)fa[(i + 1) & 1][c >> 1], (c & 1) != 0);
+          } else if constexpr (j >= 2) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int c = 8 * (j - 2) + 2 * e + z;
+              an.w[c] = widen<AF>((uint32_t)fa[0][c >> 1], (c & 1) != 0);
+            }
+          }
+          if constexpr (bj >= 0) {
+#pragma unroll
+            for (int c = 4 * e; c < 4 * e + 4; ++c)
+              fb[bj].w[c] = widen<BF>((uint32_t)rb[bj & 1][c >> 1], (c & 1) != 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        d[j] = x;
+        if constexpr (m >= 0) asm volatile("" : "+v"(acc[mi][mj]));
+        if constexpr (n == 15) {
+          rb[0] = column(2);
+          rb[1] = column(3);
+        }
+        if constexpr (j == 3) ax = an;
+        __builtin_amdgcn_sched_barrier(0);
+      });
+#pragma unroll
+      for (int j = 1; j < 4; ++j) join(acc[3][j], d[j], s[3], j);
+      read_sb(st);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   if (map.splits == 1) {
 #pragma unroll
@@ -717,12 +779,6 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
     // the sums have no use before the next step: without this they are sunk there, every product kept until then
     asm volatile("" : "+v"(c));
   };
-  auto mul = [&](const v8i& b, const v8i& a) {
-    Operand<false> x, y;
-    x.x = b;
-    y.x = a;
-    return mma<BF, AF, false>(x, y);
-  };
   // Instruction n's result stays in d[n % 4] until instruction n + 4 is due.  A step's last four results are joined
   // in the next step (tile scales), or at its end (line scales, whose columns' scales the next step replaces).
   constexpr bool kCarry = KIND == MX_FP8_TILE;
@@ -768,7 +824,7 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
         } else if constexpr (kCarry) {
           join(acc[row_of(28 + n)][col_of(28 + n)], d[n], carry[row_of(28 + n) - 5], 0);
         }
-        d[n & 3] = mul(fb[j], fa[i & 3]);
+        d[n & 3] = mma<BF, AF>(fb[j], fa[i & 3]);
         if constexpr (n >= 20 && i == 7) fb[j] = read(sB[st] + wn * kKB, j);
         if constexpr (n == 29) fa[1] = read(sA[st] + wm * kKB, 1);
         if constexpr (n == 30) fa[2] = read(sA[st] + wm * kKB, 2);

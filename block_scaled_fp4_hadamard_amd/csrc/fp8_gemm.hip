@@ -222,7 +222,7 @@ __device__ __forceinline__ const T* uniform(const T* p) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of A (single tokens and short batches): the operand that matters is
+// Few rows of A (single tokens, short batches): the operand that matters is
 // B, read once from HBM.  A workgroup takes 16 J columns of C and all M <= 16 F
 // rows; its waves take the K blocks in turn, straight from memory to registers
 // with U blocks in flight, and their sums meet in LDS in the waves' order.
@@ -623,13 +623,14 @@ __global__ void __launch_bounds__(256) fp8_mm_sum(const Fp8GemmParams p, const f
 // Rows of a tile past the operand's last line read that line again (their
 // results are not stored), so every copy stays inside the operand and any M
 // and N run here.
-constexpr int kBT = 256, kBThreads = 512, kGroupM = 4, kGroupN = 8;
+constexpr int kBT = 256, kBThreads = 512, kGroup = 32;
 constexpr int kStage = kBT * kKB;
 
 // Tiles are dealt in groups of 4 (M) x 8 (N) to the 8 XCDs, a group to the 32 CUs of one, so that the tiles
-// an XCD computes at once share 4 A strips and 8 B strips in its L2.
+// an XCD computes at once share 4 A strips and 8 B strips in its L2; 2 x 16 or 1 x 32 where there are fewer than
+// four rows of tiles.
 struct BigMap {
-  int tiles_m, tiles_n, groups_m, groups, rounds;
+  int tiles_m, tiles_n, group_m, groups_m, groups, rounds;
 };
 
 __device__ __forceinline__ int next_tile(const BigMap& t, int r, int& bm, int& bn) {
@@ -637,8 +638,8 @@ __device__ __forceinline__ int next_tile(const BigMap& t, int r, int& bm, int& b
   for (; r < t.rounds; ++r) {
     const int g = r * kXcds + xcd;
     if (g >= t.groups) return t.rounds;
-    bm = (g % t.groups_m) * kGroupM + member % kGroupM;
-    bn = (g / t.groups_m) * kGroupN + member / kGroupM;
+    bm = (g % t.groups_m) * t.group_m + member % t.group_m;
+    bn = (g / t.groups_m) * (kGroup / t.group_m) + member / t.group_m;
     if (bm < t.tiles_m && bn < t.tiles_n) return r;
   }
   return t.rounds;
@@ -860,35 +861,63 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
 }
 
 // How a product runs.  The copies of the two tiled kernels address a tile's rows by 32-bit offsets whose row pitch
-// is a 24-bit factor; operands with longer rows run on the kernel for few rows, 64 rows of A at a time.
+// is a 24-bit factor; operands with longer rows run on the kernel for few rows, 32 rows of A at a time.
 enum class Path { kFew, kMid, kBig };
 
 struct Plan {
   Path path;
   int splits;
+  BigMap big;
 };
 
+BigMap big_map(int64_t M, int64_t N) {
+  BigMap map;
+  map.tiles_m = (int)((M + kBT - 1) / kBT);
+  map.tiles_n = (int)((N + kBT - 1) / kBT);
+  map.group_m = map.tiles_m >= 3 ? 4 : map.tiles_m;
+  map.groups_m = (map.tiles_m + map.group_m - 1) / map.group_m;
+  const int group_n = kGroup / map.group_m;
+  map.groups = map.groups_m * ((map.tiles_n + group_n - 1) / group_n);
+  map.rounds = (map.groups + kXcds - 1) / kXcds;
+  return map;
+}
+
+// By measurement (bf16 output, tile scales): up to 32 rows of A, reading B once wins (16 x 6144 x 4096: 10 us
+// against 16; 64 rows: 22 against 16).  Above, a K block of a full round of the chip costs about 1.67 us in 256 x 256
+// tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU, half the work; about 0.7 us with one a CU), and the fewest
+// such times win.  fp32 output always takes the small tiles, whose wave leaves room for the widened operands.  Where
+// small tiles fill less than half of their 512 places, a tile's K blocks are split, at least four to a part.
 Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lda_scales, int64_t ldb_scales,
              int out_kind) {
+  Plan plan{Path::kFew, 1, {}};
   const int64_t lim = int64_t(1) << 24;
-  if (M <= 64 || lda >= lim || ldb >= lim || lda_scales >= lim || ldb_scales >= lim) return {Path::kFew, 1};
+  if (M <= 32 || lda >= lim || ldb >= lim || lda_scales >= lim || ldb_scales >= lim) return plan;
   const int64_t nk = (K + kKB - 1) / kKB;
-  const int64_t big = ((M + kBT - 1) / kBT) * ((N + kBT - 1) / kBT);
-  if (out_kind == MX_OUT_BF16 && big >= 192) return {Path::kBig, 1};
   const int64_t tiles = ((M + kMT - 1) / kMT) * ((N + kMT - 1) / kMT);
-  int64_t splits = 1;
-  while (tiles * splits * 2 <= 512 && nk >= 8 * splits * 2) splits *= 2;
-  return {Path::kMid, (int)splits};
+  plan.path = Path::kMid;
+  if (tiles <= 256) {
+    plan.splits = (int)(512 / tiles < nk / 4 ? 512 / tiles : nk / 4);
+    if (plan.splits < 1) plan.splits = 1;
+    return plan;
+  }
+  if (out_kind == MX_OUT_BF16) {
+    plan.big = big_map(M, N);
+    const double rest = (double)(tiles % 512);
+    const double mid = 1.15 * (double)(tiles / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.7 : 1.15);
+    if (1.67 * plan.big.rounds < mid) plan.path = Path::kBig;
+  }
+  return plan;
 }
 
 template <int AF, int BF, int KIND, int OUT, int F>
 void launch_few(const Fp8GemmParams& p, hipStream_t s) {
-  for (int64_t m = 0; m < p.M; m += 64) {
+  for (int64_t m = 0; m < p.M; m += 16 * F) {
     Fp8GemmParams r = p;
     r.a_codes += m * p.lda;
     r.a_scales += m;
-    r.M = p.M - m < 64 ? p.M - m : 64;
+    r.M = p.M - m < 16 * F ? p.M - m : 16 * F;
     r.c = (uint8_t*)p.c + m * p.ldc * (OUT == MX_OUT_F32 ? 4 : 2);
+    // two column fragments a workgroup where that leaves one for every CU
     if (p.N >= 32 * 256)
       hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, 2>), dim3((unsigned)((p.N + 31) / 32)),
                          dim3(64 * kFewWaves), 0, s, r);
@@ -903,19 +932,12 @@ void launch(const Fp8GemmParams& p, float* parts, int64_t parts_bytes, hipStream
   Plan plan = plan_of(p.M, p.N, p.K, p.lda, p.ldb, p.lda_scales, p.ldb_scales, OUT);
   if (plan.path == Path::kFew) {
     if (p.M <= 16) launch_few<AF, BF, KIND, OUT, 1>(p, s);
-    else if (p.M <= 32) launch_few<AF, BF, KIND, OUT, 2>(p, s);
-    else launch_few<AF, BF, KIND, OUT, 4>(p, s);
+    else launch_few<AF, BF, KIND, OUT, 2>(p, s);
     return;
   }
   if constexpr (OUT == MX_OUT_BF16) {
     if (plan.path == Path::kBig) {
-      BigMap map;
-      map.tiles_m = (int)((p.M + kBT - 1) / kBT);
-      map.tiles_n = (int)((p.N + kBT - 1) / kBT);
-      map.groups_m = (map.tiles_m + kGroupM - 1) / kGroupM;
-      map.groups = map.groups_m * ((map.tiles_n + kGroupN - 1) / kGroupN);
-      map.rounds = (map.groups + kXcds - 1) / kXcds;
-      hipLaunchKernelGGL((fp8_mm_big<AF, BF, KIND>), dim3(kXcds * kGroupM * kGroupN), dim3(kBThreads), 0, s, p, map);
+      hipLaunchKernelGGL((fp8_mm_big<AF, BF, KIND>), dim3(kXcds * kGroup), dim3(kBThreads), 0, s, p, plan.big);
       return;
     }
   }

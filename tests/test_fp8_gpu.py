@@ -147,7 +147,7 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (1, 1000, 300), (2, 130, 129), (5, 4096, 512)
           (17, 65, 257), (31, 1003, 640), (33, 300, 1000), (64, 256, 14336), (65, 500, 384), (100, 1, 700),
           (128, 128, 128), (129, 127, 255), (255, 257, 600), (256, 256, 256), (300, 1003, 1001), (512, 768, 640),
           (700, 520, 2000), (1000, 1300, 385),
-          (4200, 4300, 300)]
+          (4200, 4300, 300), (4000, 8100, 300), (256, 33000, 128), (500, 17000, 200), (40, 200, 9000), (300, 500, 4100)]
 
 
 @pytest.mark.parametrize("kind", ["line", "tile"])
@@ -220,6 +220,96 @@ def test_nan_blocks_reach_only_their_rows_and_columns():
         bad = torch.zeros_like(c, dtype=torch.bool)
         bad[1], bad[:, 5] = True, True
         assert torch.equal(torch.isnan(c), bad)
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 33, 300), (70, 20, 130)])
+def test_rows_far_apart(m, n, k):
+    """Operand rows and scale rows 2^24 bytes and floats apart: the same numbers as close together, with offsets that
+    pass 31 bits."""
+    rng = np.random.default_rng(16)
+    for kind in ("line", "tile"):
+        _, qa = operand(m, k, "line", "e4m3", rng)
+        _, qb = operand(n, k, kind, "e4m3", rng)
+
+        def apart(q):
+            codes = torch.zeros((q.codes.shape[0], 1 << 24), dtype=torch.uint8, device="cuda")[:, :q.codes.shape[1]]
+            codes.copy_(q.codes)
+            scales = torch.zeros((q.scales.shape[0], 1 << 24), device="cuda")[:, :q.scales.shape[1]]
+            scales.copy_(q.scales)
+            return Fp8Tensor(codes, scales, q.k, q.fmt, q.kind)
+        announce("fp8 rows far apart %s" % kind)
+        for dtype in (torch.float32, torch.bfloat16):
+            got = fp8_gemm(apart(qa), apart(qb), out_dtype=dtype)
+            torch.cuda.synchronize()
+            assert_product(got, (qa.codes.cpu().numpy(), qa.scales.cpu().numpy()), "e4m3",
+                           (qb.codes.cpu().numpy(), qb.scales.cpu().numpy()), "e4m3", kind, dtype == torch.bfloat16,
+                           (m, n, k, kind))
+
+
+def test_cast_of_a_large_matrix():
+    """More than 2^31 elements: the last rows and columns of each output are those of the same rows cast alone."""
+    rows, cols = 131072 + 128, 16400
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x[-256:] = torch.randn((256, cols), generator=gen, device="cuda").bfloat16()
+    announce("fp8 cast of a large matrix")
+    q = fp8_quantize(x, axis="both")
+    tail = fp8_quantize(x[-256:].contiguous(), axis="both")
+    assert torch.equal(q["row"].codes[-256:], tail["row"].codes) and torch.equal(q["row"].scales[:, -256:], tail["row"].scales)
+    assert torch.equal(q["col"].codes[:, -256:], tail["col"].codes) and torch.equal(q["col"].scales[-2:], tail["col"].scales)
+    assert int(q["row"].codes[:1000].max()) == 0 and int(q["col"].codes[-1, :1000].max()) == 0
+
+
+def test_split_products_at_once_and_replayed():
+    """Products whose K is split over workgroups: two at once on two streams, each with its workspace, and two captured
+    graphs replayed in turn and at once, with eager products between: every result is the eager one's, bit for bit.  A
+    smaller or no workspace gives fewer parts and the same numbers within the accumulation bound."""
+    from block_scaled_fp4_hadamard_amd import _lib
+    rng = np.random.default_rng(17)
+    m, n, k = 300, 500, 8192
+    assert _lib.mx_fp8_gemm_workspace(m, n, k, 1) > 4 * m * n
+    ops = [(operand(m, k, "line", "e4m3", rng), operand(n, k, "tile", "e4m3", rng)) for _ in range(2)]
+    want = [[fp8_gemm(a[1], b[1], out_dtype=d) for a, b in ops] for d in (torch.bfloat16, torch.float32)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty((m, n), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    announce("fp8 split products on two streams")
+    for i, s in enumerate(streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                fp8_gemm(ops[i][0][1], ops[i][1][1], out=outs[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0][0]) and torch.equal(outs[1], want[0][1])
+    announce("fp8 split products in graphs")
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fp8_gemm(ops[i][0][1], ops[i][1][1], out=outs[i])
+        graphs.append(g)
+    for turn in range(3):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        again = fp8_gemm(ops[turn % 2][0][1], ops[turn % 2][1][1])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0][0]) and torch.equal(outs[1], want[0][1])
+        assert torch.equal(again, want[1][turn % 2])
+    (a, qa), (b, qb) = ops[0]
+    full = _lib.mx_fp8_gemm_workspace(m, n, k, 0)
+    for size in (full // 2, 0):
+        announce("fp8 split product with %d bytes" % size)
+        space = torch.full((max(size, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+        c = torch.empty((m, n), device="cuda")
+        _lib.check(_lib.mx_fp8_gemm(qa.c_struct(), 0, qb.c_struct(), 0, 1, m, n, k, c.data_ptr(), n, 0,
+                                    space.data_ptr() if size else None, size, torch.cuda.current_stream().cuda_stream),
+                   "mx_fp8_gemm")
+        torch.cuda.synchronize()
+        assert_product(c, a, "e4m3", b, "e4m3", "tile", False, size)
 
 
 def test_empty_products():

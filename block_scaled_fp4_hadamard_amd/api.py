@@ -333,13 +333,15 @@ def _launch(dev, name, entry, *args):
     """entry(*args, stream) on dev's current stream, with dev the current device; host tensors are refused."""
     if dev.type != "cuda":
         raise ValueError("the operands must be CUDA tensors, got %s" % dev)
-    stream = torch._C._cuda_getCurrentRawStream(dev.index) or None
-    if dev.index == torch.cuda.current_device():
+    at = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(at) or None
+    if at == torch.cuda.current_device():
         st = entry(*args, stream)
     else:
         with torch.cuda.device(dev):
             st = entry(*args, stream)
-    _lib.check(st, name)
+    if st:
+        raise _lib.MXError(st, name)
 
 
 @dataclass
@@ -407,20 +409,24 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
     dev = x.device
     out = {}
     c = [None, None]
-    for i, (name, given, lines, k) in enumerate((("row", row_out, rows, cols), ("col", col_out, cols, rows))):
-        if axis != name and axis != "both":
-            continue
-        q = given
-        if q is None:
-            q = empty_fp8(lines, k, dev, fmt, kind)
-        elif (q.lines, q.k, q.fmt, q.kind) != (lines, k, fmt, kind) or q.codes.device != dev:
-            raise ValueError("%s_out is not an %s operand of %d %s lines of %d values on %s"
-                             % (name, fmt, lines, kind, k, dev))
-        out[name] = q
-        c[i] = q.check(name + "_out")
-    _launch(dev, "mx_fp8_quantize", _lib.mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _lib.FP8_FMT[fmt],
+    if axis != "col":
+        q = row_out if row_out is not None else empty_fp8(rows, cols, dev, fmt, kind)
+        out["row"], c[0] = q, _fp8_output(q, row_out is not None, "row_out", rows, cols, fmt, kind, dev)
+    if axis != "row":
+        q = col_out if col_out is not None else empty_fp8(cols, rows, dev, fmt, kind)
+        out["col"], c[1] = q, _fp8_output(q, col_out is not None, "col_out", cols, rows, fmt, kind, dev)
+    _launch(dev, "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _lib.FP8_FMT[fmt],
             _lib.FP8_KIND[kind], _lib.AXIS[axis], *c)
     return out
+
+
+def _fp8_output(q, given, name, lines, k, fmt, kind, dev):
+    """An output operand as the library takes it: checked if it is the caller's, plain if it was made just now."""
+    if not given:
+        return _lib.Fp8TensorC(q.codes.data_ptr(), q.codes.shape[1], q.scales.data_ptr(), q.scales.shape[1])
+    if (q.lines, q.k, q.fmt, q.kind) != (lines, k, fmt, kind) or q.codes.device != dev:
+        raise ValueError("%s is not an %s operand of %d %s lines of %d values on %s" % (name, fmt, lines, kind, k, dev))
+    return q.check(name)
 
 
 def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
@@ -449,7 +455,7 @@ def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
     # the workspace is this call's own: held until the launch, its memory then goes to later work of this stream only
     size = _lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
     space = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _launch(dev, "mx_fp8_gemm", _lib.mx_fp8_gemm, ca, _lib.FP8_FMT[a.fmt], cb, _lib.FP8_FMT[b.fmt],
+    _launch(dev, "mx_fp8_gemm", _lib.lib().mx_fp8_gemm, ca, _lib.FP8_FMT[a.fmt], cb, _lib.FP8_FMT[b.fmt],
             _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), ldc, kind,
             space.data_ptr() if size else None, size)
     return out
@@ -576,4 +582,4 @@ def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
     if dev is None:
         _lib.check(_lib.mx_adamw_step(*args, None), "mx_adamw_step")       # an empty list: only the checks run
     else:
-        _launch(dev, "mx_adamw_step", _lib.mx_adamw_step, *args)
+        _launch(dev, "mx_adamw_step", _lib.lib().mx_adamw_step, *args)

@@ -124,7 +124,7 @@ typedef v4f v4f_any __attribute__((aligned(4)));
 // bf16: lanes l and l ^ 8 trade halves of their 32 bytes, so that each store writes whole 128-byte pieces of
 // eight rows.  fp32: each quad of lanes transposes its 4 x 4 pieces of 16 bytes, so that each store writes
 // whole 256-byte pieces of four rows (a lane's own 64 bytes, stored as they are, reached 0.9 TB/s).  The last
-// columns of an odd width go one by one.  KEEP: sums that are read again soon stay in the caches.
+// columns of an odd width go one by one.
 __device__ __forceinline__ float dpp_xor1(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
 }
@@ -132,7 +132,7 @@ __device__ __forceinline__ float dpp_xor2(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
 }
 
-template <int OUT, bool KEEP = false>
+template <int OUT>
 __device__ __forceinline__ void store_rows(const Fp8GemmParams& p, int64_t m0, int64_t n0, int lane,
                                            const v4f (&acc)[4]) {
   const int lrow = lane & 15, q = lane >> 4;
@@ -163,8 +163,7 @@ __device__ __forceinline__ void store_rows(const Fp8GemmParams& p, int64_t m0, i
       if (m >= p.M) continue;
       float* c = (float*)p.c + m * p.ldc + n;
       if (n + 4 <= p.N) {
-        if constexpr (KEEP) *(v4f_any*)c = t[e];
-        else __builtin_nontemporal_store(t[e], (v4f_any*)c);
+        __builtin_nontemporal_store(t[e], (v4f_any*)c);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -571,7 +570,7 @@ __global__ void __launch_bounds__(kMThreads, 2) fp8_mm_mid(const Fp8GemmParams p
     w.c = map.parts + (int64_t)split * p.M * p.N;
     w.ldc = p.N;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store_rows<MX_OUT_F32, true>(w, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
+    for (int i = 0; i < 4; ++i) store_rows<MX_OUT_F32>(w, m0 + wm + 16 * i, n0 + wn, lane, acc[i]);
   }
 }
 
@@ -882,11 +881,32 @@ BigMap big_map(int64_t M, int64_t N) {
   return map;
 }
 
+// Into how many parts the K blocks of at most 256 small tiles are split: the least time by what was measured (us).  A
+// K block takes 0.55 to 0.68 (fp32 output: 1.0) while every CU has one workgroup at most, 0.8 to 0.9 (1.6) with two;
+// the parts' float32 sums cost 0.45 a megabyte, written and read back, and the second launch 4.5.  1000 x 2000 x 2048:
+// 14 us whole, 20 in two parts; 400 x 2000 x 8192: 44 whole, 23 in four; 333 x 4096 x 14336: 70 whole, 37 in five.
+int best_splits(int64_t tiles, int64_t nk, double outputs, bool exact) {
+  int best = 1;
+  double least = 0.0;
+  for (const int splits : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64}) {
+    const int64_t all = tiles * splits;
+    if (splits > 1 && (all > 512 || splits * 2 > nk)) break;
+    const double block = exact ? (all <= 256 ? 1.0 : 1.6)
+                               : (all <= 256 ? 0.55 + 0.13 * (double)all / 256 : 0.7 + 0.1 * (double)all / 256);
+    const double us = block * (double)((nk + splits - 1) / splits) +
+                      (splits > 1 ? 4.5 + 0.45e-6 * 4.0 * outputs * splits : 0.0);
+    if (splits == 1 || us < least) {
+      best = splits;
+      least = us;
+    }
+  }
+  return best;
+}
+
 // By measurement (bf16 output, tile scales): up to 32 rows of A, reading B once wins (16 x 6144 x 4096: 10 us
 // against 16; 64 rows: 22 against 16).  Above, a K block of a full round of the chip costs about 1.67 us in 256 x 256
 // tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU, half the work; about 0.7 us with one a CU), and the fewest
-// such times win.  fp32 output always takes the small tiles, whose wave leaves room for the widened operands.  Where
-// small tiles fill less than half of their 512 places, a tile's K blocks are split, at least four to a part.
+// such times win.  fp32 output always takes the small tiles, whose wave leaves room for the widened operands.
 Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lda_scales, int64_t ldb_scales,
              int out_kind) {
   Plan plan{Path::kFew, 1, {}};
@@ -896,8 +916,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t 
   const int64_t tiles = ((M + kMT - 1) / kMT) * ((N + kMT - 1) / kMT);
   plan.path = Path::kMid;
   if (tiles <= 256) {
-    plan.splits = (int)(512 / tiles < nk / 4 ? 512 / tiles : nk / 4);
-    if (plan.splits < 1) plan.splits = 1;
+    plan.splits = best_splits(tiles, nk, (double)M * (double)N, out_kind == MX_OUT_F32);
     return plan;
   }
   if (out_kind == MX_OUT_BF16) {

@@ -502,7 +502,6 @@ mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t b
   if (count < 0 || (count > 0 && tensors == nullptr) || params == nullptr) return MX_ERR_INVALID;
   if (bits != 8 && bits != 32) return MX_ERR_INVALID;
   if (round != MX_ROUND_RTNE && round != MX_ROUND_SR) return MX_ERR_INVALID;
-  if (bits == 32 && round != MX_ROUND_RTNE) return MX_ERR_INVALID;
   const mx_adamw_params& q = *params;
   if (!(q.beta1 >= 0.0 && q.beta1 < 1.0) || !(q.beta2 >= 0.0 && q.beta2 < 1.0)) return MX_ERR_INVALID;
   if (!(q.eps >= 0.0) || !isfinite(q.eps) || !isfinite(q.weight_decay)) return MX_ERR_INVALID;

@@ -463,8 +463,8 @@ int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out);
  *              captured graph can be replayed with a step that moves on
  *   lr         likewise, or the float32 at lr_dev
  *   grad_scale NULL, or a device float32 (the clipping or loss-scale factor)
- *   round      MX_ROUND_RTNE; MX_ROUND_SR with bits 8 only
- *   seed       keys the draws; pass another one each step
+ *   round      how 8-bit moments are cast (no meaning with bits 32)
+ *   seed       keys the draws of MX_ROUND_SR; pass another one each step
  */
 typedef struct {
   float *w;

@@ -316,6 +316,7 @@ def _fp8_blocks(n):
     return -(-n // FP8_BLOCK)
 
 
+_FP8_FMT, _FP8_KIND, _Fp8TensorC = _lib.FP8_FMT, _lib.FP8_KIND, _lib.Fp8TensorC
 _OUT_KINDS = {torch.float32: _lib.OUT["f32"], torch.bfloat16: _lib.OUT["bf16"]}
 
 
@@ -329,16 +330,16 @@ def _pitch(stride, rows, cols, name):
     return ld if rows > 1 else cols
 
 
-def _launch(dev, name, entry, *args):
-    """entry(*args, stream) on dev's current stream, with dev the current device; host tensors are refused."""
-    if dev.type != "cuda":
-        raise ValueError("the operands must be CUDA tensors, got %s" % dev)
-    at = dev.index
+def _launch(at, name, entry, *args):
+    """entry(*args, stream) on the current stream of CUDA device number `at`, as the current device; a number below 0,
+    a host tensor's, is refused."""
+    if at < 0:
+        raise ValueError("the operands must be CUDA tensors")
     stream = torch._C._cuda_getCurrentRawStream(at) or None
     if at == torch.cuda.current_device():
         st = entry(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(at):
             st = entry(*args, stream)
     if st:
         raise _lib.MXError(st, name)
@@ -364,21 +365,21 @@ class Fp8Tensor:
 
     def check(self, name):
         """The operand as the library takes it; ValueError if its tensors are not what the class describes."""
-        codes, scales = self.codes, self.scales
-        if self.fmt not in _lib.FP8_FMT or self.kind not in _lib.FP8_KIND:
-            raise ValueError("%s: unknown format %r or kind %r" % (name, self.fmt, self.kind))
-        kb = _fp8_blocks(self.k)
-        shape, sshape = codes.shape, scales.shape
-        if codes.dtype != torch.uint8 or len(shape) != 2 or shape[1] != kb * FP8_BLOCK:
-            raise ValueError("%s: codes must be uint8 (lines, %d) for k = %d" % (name, kb * FP8_BLOCK, self.k))
+        codes, scales, kind = self.codes, self.scales, self.kind
+        if self.fmt not in _FP8_FMT or kind not in _FP8_KIND:
+            raise ValueError("%s: unknown format %r or kind %r" % (name, self.fmt, kind))
+        kb = -(-self.k // 128)
+        shape = codes.shape
+        if codes.dtype != torch.uint8 or len(shape) != 2 or shape[1] != kb * 128:
+            raise ValueError("%s: codes must be uint8 (lines, %d) for k = %d" % (name, kb * 128, self.k))
         lines, width = shape
-        rows, cols = (kb, lines) if self.kind == "line" else (_fp8_blocks(lines), kb)
-        if scales.dtype != torch.float32 or len(sshape) != 2 or sshape[0] != rows or sshape[1] != cols:
-            raise ValueError("%s: scales must be float32 %s for kind %r" % (name, (rows, cols), self.kind))
-        if scales.device != codes.device:
+        rows, cols = (kb, lines) if kind == "line" else (-(-lines // 128), kb)
+        if scales.dtype != torch.float32 or scales.shape != (rows, cols):
+            raise ValueError("%s: scales must be float32 %s for kind %r" % (name, (rows, cols), kind))
+        if scales.get_device() != codes.get_device():
             raise ValueError("%s: codes and scales are on different devices" % name)
-        return _lib.Fp8TensorC(codes.data_ptr(), _pitch(codes.stride(), lines, width, name),
-                               scales.data_ptr(), _pitch(scales.stride(), rows, cols, name))
+        return _Fp8TensorC(codes.data_ptr(), _pitch(codes.stride(), lines, width, name),
+                           scales.data_ptr(), _pitch(scales.stride(), rows, cols, name))
 
     def c_struct(self):
         return self.check("operand")
@@ -415,7 +416,7 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
     if axis != "row":
         q = col_out if col_out is not None else empty_fp8(cols, rows, dev, fmt, kind)
         out["col"], c[1] = q, _fp8_output(q, col_out is not None, "col_out", cols, rows, fmt, kind, dev)
-    _launch(dev, "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _lib.FP8_FMT[fmt],
+    _launch(x.get_device(), "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _lib.FP8_FMT[fmt],
             _lib.FP8_KIND[kind], _lib.AXIS[axis], *c)
     return out
 
@@ -440,24 +441,23 @@ def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
         raise ValueError("operands disagree on K: %d vs %d" % (a.k, b.k))
     if a.kind != "line":
         raise ValueError("a must be scaled by lines, got kind %r" % a.kind)
-    dev = a.codes.device
+    at = a.codes.get_device()
     M, N = a.codes.shape[0], b.codes.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = a.codes.new_empty((M, N), dtype=out_dtype)
     elif out.dim() != 2 or out.shape[0] != M or out.shape[1] != N:
         raise ValueError("out must be a row-major (%d, %d) view" % (M, N))
     kind = _OUT_KINDS.get(out.dtype)
     if kind is None:
         raise ValueError("the output must be float32 or bfloat16, got %s" % out.dtype)
-    if b.codes.device != dev or out.device != dev:
+    if b.codes.get_device() != at or out.get_device() != at:
         raise ValueError("a, b and out must be on one device")
-    ldc = _pitch(out.stride(), M, N, "out")
+    lib = _lib.lib()
     # the workspace is this call's own: held until the launch, its memory then goes to later work of this stream only
-    size = _lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
-    space = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _launch(dev, "mx_fp8_gemm", _lib.lib().mx_fp8_gemm, ca, _lib.FP8_FMT[a.fmt], cb, _lib.FP8_FMT[b.fmt],
-            _lib.FP8_KIND[b.kind], M, N, a.k, out.data_ptr(), ldc, kind,
-            space.data_ptr() if size else None, size)
+    size = lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
+    space = a.codes.new_empty(size) if size else None
+    _launch(at, "mx_fp8_gemm", lib.mx_fp8_gemm, ca, _FP8_FMT[a.fmt], cb, _FP8_FMT[b.fmt], _FP8_KIND[b.kind], M, N, a.k,
+            out.data_ptr(), _pitch(out.stride(), M, N, "out"), kind, space.data_ptr() if size else None, size)
     return out
 
 
@@ -582,4 +582,4 @@ def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
     if dev is None:
         _lib.check(_lib.mx_adamw_step(*args, None), "mx_adamw_step")       # an empty list: only the checks run
     else:
-        _launch(dev, "mx_adamw_step", _lib.lib().mx_adamw_step, *args)
+        _launch(dev.index if dev.type == "cuda" else -1, "mx_adamw_step", _lib.lib().mx_adamw_step, *args)

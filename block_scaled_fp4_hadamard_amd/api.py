@@ -321,7 +321,7 @@ _OUT_KINDS = {torch.float32: _lib.OUT["f32"], torch.bfloat16: _lib.OUT["bf16"]}
 
 
 def _pitch(stride, rows, cols, name):
-    """Elements between the rows of a rows x cols tensor of this stride: unit column stride, rows that do not overlap."""
+    """Elements between the rows of a rows x cols tensor of this stride, whose rows are whole and do not overlap."""
     ld, one = stride
     if cols > 1 and one != 1:
         raise ValueError("%s must have unit column stride" % name)
@@ -416,8 +416,8 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
     if axis != "row":
         q = col_out if col_out is not None else empty_fp8(cols, rows, dev, fmt, kind)
         out["col"], c[1] = q, _fp8_output(q, col_out is not None, "col_out", cols, rows, fmt, kind, dev)
-    _launch(x.get_device(), "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _lib.FP8_FMT[fmt],
-            _lib.FP8_KIND[kind], _lib.AXIS[axis], *c)
+    _launch(x.get_device(), "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _FP8_FMT[fmt],
+            _FP8_KIND[kind], _lib.AXIS[axis], *c)
     return out
 
 

@@ -390,7 +390,8 @@ typedef struct {
  *   fmt, kind  of every output
  *   axis       which outputs: row_out holds rows lines of length cols, col_out
  *              the transpose, cols lines of length rows; both come from one
- *              read of x, and MX_FP8_TILE gives both the same scales
+ *              read of x, and MX_FP8_TILE gives both the same scales.  They
+ *              must not overlap x or one another
  */
 mx_status mx_fp8_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld_x, mx_fp8_fmt fmt,
                           mx_fp8_kind kind, mx_axis axis, const mx_fp8_tensor *row_out,
@@ -458,6 +459,7 @@ int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out);
  *              arrays of all entries must not overlap, and each is aligned to
  *              its element (w, m, v, g, copy 16-byte aligned, 8-bit m and v
  *              8-byte aligned: fastest)
+ *   eps        >= 0; with eps 0 an element whose moments are both 0 becomes NaN
  *   step       t >= 1; if step_dev is not NULL the device's int64 is read
  *              instead when the kernel runs (it must be >= 1), so that a
  *              captured graph can be replayed with a step that moves on

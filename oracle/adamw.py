@@ -7,8 +7,8 @@ float64.  8-bit moments have a float32 scale for each 128 elements of the flatte
 second in E5M3 (5 exponent bits, 3 mantissa bits, bias 15, no sign; codes up to 0xF7 = 61440).  A moment is
 code * scale; after the step s = max(RN32(amax * RN32(1 / F)), 2^-126), F = 448 or 61440, and
 y = RN32(value * RN32(1 / s)) goes to the nearest level, ties to the even code, or up from the level below iff
-floor(f 2^16) + r >= 2^16 with f the fraction of the step and r the element's 16-bit draw.  A second moment above 0 keeps at least code 1; a block holding
-Inf or NaN gets s = NaN and codes 0.
+floor(f 2^16) + r >= 2^16 with f the fraction of the step and r the element's 16-bit draw.  A second moment above 0
+keeps at least code 1; a block holding Inf or NaN gets s = NaN and codes 0.
 """
 import numpy as np
 

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams
     v4f cb[U][J];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      // a block past the last reads the last again and counts nothing
+      // a block past the last reads the last again and is left out below
       const int64_t k = kb + u * kFewWaves < nk ? kb + u * kFewWaves : nk - 1;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float s = ca[u][f] * cb[u][j][KIND == MX_FP8_TILE ? 0 : r];
-            acc[f][j][r] = fmaf(d[r], counts ? s : 0.0f, acc[f][j][r]);
+            // chosen, not multiplied by 0: the block may hold Inf
+            acc[f][j][r] = counts ? fmaf(d[r], s, acc[f][j][r]) : acc[f][j][r];
           }
         }
       }

@@ -350,3 +350,31 @@ def test_streams_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(c, want[i])
         assert torch.equal(fp8_gemm(fp8_quantize(xs[i])["row"], qw), want[i])
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["line", "tile"])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 650), (20, 9000, 130), (40, 300, 1100), (200, 130, 128)])
+def test_infinities_stay_infinite(M, N, K, kind, bf16):
+    """An E5M2 Inf code or an Inf scale in a line's last block gives that line Inf, a NaN scale NaN, the others nothing,
+    whatever the number of blocks.  All values are positive, so that no Inf meets its negative."""
+    rng = np.random.default_rng(M + N)
+    (ac, asc), _ = operand(M, K, "line", "e5m2", rng)
+    (bc, bsc), _ = operand(N, K, kind, "e4m3", rng)
+    ac &= 0x7F
+    bc &= 0x7F
+    bc[:, K - 1] = 0x38            # 1
+    ac[:3, K - 1] = 0x3C           # 1
+    clean = ac.copy(), asc.copy()
+    ac[0, K - 1] = 0x7C
+    asc[-1, 1], asc[-1, 2] = np.inf, np.nan
+    a = Fp8Tensor(torch.from_numpy(ac).cuda(), torch.from_numpy(asc).cuda(), K, "e5m2", "line")
+    b = Fp8Tensor(torch.from_numpy(bc).cuda(), torch.from_numpy(bsc).cuda(), K, "e4m3", kind)
+    announce("fp8 infinities %dx%dx%d %s %s" % (M, N, K, kind, "bf16" if bf16 else "fp32"))
+    got = fp8_gemm(a, b, torch.bfloat16 if bf16 else torch.float32)
+    torch.cuda.synchronize()
+    assert bool((got[:2] == float("inf")).all())
+    assert bool(got[2].isnan().all())
+    if M > 3:
+        rest = tuple(np.ascontiguousarray(x) for x in (clean[0][3:], clean[1][:, 3:]))
+        assert_product(got[3:], rest, "e5m2", (bc, bsc), "e4m3", kind, bf16, "rest")

@@ -42,6 +42,7 @@ namespace {
 constexpr int kAwThreads = 512;
 constexpr int kAwChunk = 8 * kAwThreads;
 constexpr unsigned kAwGrid = 1024;         // 4 workgroups on each of the 256 CUs
+constexpr unsigned kAwMost = 1u << 22;     // a grid holds fewer than 2^32 threads; the workgroups take more chunks in turn
 
 struct AdamwArgs {
   AdamwTensor t[kAdamwGroup];
@@ -272,10 +273,9 @@ __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const AdamwArgs a) {
 }
 
 // every array of the tensor may be read and written eight elements at a time
-bool vectors(const AdamwTensor& t, bool grad_bf16, int bits) {
+bool vectors(const AdamwTensor& t, int bits) {
   const uintptr_t wide = (uintptr_t)t.w | (uintptr_t)t.g | (uintptr_t)t.copy;
   const uintptr_t state = (uintptr_t)t.m | (uintptr_t)t.v;
-  (void)grad_bf16;
   return wide % 16 == 0 && state % (bits == 8 ? 8 : 16) == 0;
 }
 
@@ -294,13 +294,14 @@ hipError_t launch_adamw(const AdamwTensor* tensors, const bool* grad_bf16, int c
     if (i < count) chunks += (uint32_t)((a.t[i].n + kAwChunk - 1) / kAwChunk);
     a.end[i] = chunks;
     const bool bf = grad_bf16[i < count ? i : count - 1];
-    a.flags[i] = (uint8_t)((bf ? 1 : 0) | (vectors(a.t[i], bf, bits) ? 2 : 0));
+    a.flags[i] = (uint8_t)((bf ? 1 : 0) | (vectors(a.t[i], bits) ? 2 : 0));
   }
   if (chunks == 0) return hipSuccess;
   // one workgroup a chunk (5.4 TB/s on a block's weights against 5.0 with a resident grid); where each workgroup forms
   // the coefficients itself, a resident grid, so that the few thousand instructions of it are paid once
   const bool form = step.step_dev != nullptr || step.lr_dev != nullptr;
-  const dim3 g(form && chunks > kAwGrid ? kAwGrid : chunks), b(kAwThreads);
+  const unsigned most = form ? kAwGrid : kAwMost;
+  const dim3 g(chunks < most ? chunks : most), b(kAwThreads);
   if (bits == 32) hipLaunchKernelGGL((adamw_kernel<32, MX_ROUND_RTNE>), g, b, 0, s, a);
   else if (round == MX_ROUND_SR) hipLaunchKernelGGL((adamw_kernel<8, MX_ROUND_SR>), g, b, 0, s, a);
   else hipLaunchKernelGGL((adamw_kernel<8, MX_ROUND_RTNE>), g, b, 0, s, a);

@@ -163,10 +163,10 @@ mx_status check_fp8(const mx_fp8_tensor* q, int64_t lines, int64_t k, int kind) 
   return MX_OK;
 }
 
-// more 128 x 128 tiles than one launch's grid can number
+// 128 x 128 tiles that one launch can take: its grid holds fewer than 2^32 threads, 256 a tile
 bool too_many_tiles(int64_t m, int64_t n) {
-  return fp8_blocks(m) >= (int64_t(1) << 31) || fp8_blocks(n) >= (int64_t(1) << 31) ||
-         fp8_blocks(m) * fp8_blocks(n) >= (int64_t(1) << 31);
+  constexpr int64_t kMost = int64_t(1) << 23;
+  return fp8_blocks(m) >= kMost || fp8_blocks(n) >= kMost || fp8_blocks(m) * fp8_blocks(n) >= kMost;
 }
 
 }  // namespace
@@ -471,7 +471,9 @@ mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_ten
   s = check_fp8(b, N, K, b_kind);
   if (s != MX_OK) return s;
   const uintptr_t esize = out == MX_OUT_F32 ? 4u : 2u;
-  if (c == nullptr || ((uintptr_t)c % esize) != 0 || ldc < N || too_many_tiles(M, N)) return MX_ERR_INVALID;
+  if (c == nullptr || ((uintptr_t)c % esize) != 0 || ldc < N) return MX_ERR_INVALID;
+  // few rows: 512 threads for each 32 columns
+  if (too_many_tiles(M, N) || N >= (int64_t(1) << 27)) return MX_ERR_INVALID;
   if (workspace_bytes < 0 || !aligned16(workspace)) return MX_ERR_INVALID;
   mx::Fp8GemmParams p{};
   p.a_codes = a->codes;
@@ -511,7 +513,7 @@ mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t b
   const uintptr_t state = bits == 32 ? 3u : 0u;
   for (int32_t i = 0; i < count; ++i) {
     const mx_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.n >= (int64_t(1) << 40)) return MX_ERR_INVALID;
+    if (t.n < 0 || t.n >= (int64_t(1) << 36)) return MX_ERR_INVALID;
     if (t.grad != MX_OUT_F32 && t.grad != MX_OUT_BF16) return MX_ERR_INVALID;
     if (t.n == 0) continue;
     if (t.w == nullptr || t.g == nullptr || t.m == nullptr || t.v == nullptr) return MX_ERR_INVALID;

@@ -384,9 +384,9 @@ typedef struct {
  *   s = max(RN32(amax * RN32(1 / F)), 2^-126), F = 448 or 57344;  r = RN32(1 / s);
  *   code = RN32(x * r) rounded to nearest even in the format.
  * A block holding Inf or NaN gets s = NaN and codes 0.
- *   x, rows, cols, ld_x  device, 16-byte aligned bf16 bit patterns; any rows,
+ *   x, rows, cols, ld_x  device, 16-byte aligned bf16 bit patterns;
  *              cols % 8 == 0, ld_x >= cols and a multiple of 8; either size
- *              0: nothing to do, MX_OK
+ *              0: nothing to do, MX_OK; fewer than 2^23 tiles of 128 x 128
  *   fmt, kind  of every output
  *   axis       which outputs: row_out holds rows lines of length cols, col_out
  *              the transpose, cols lines of length rows; both come from one
@@ -409,7 +409,8 @@ mx_status mx_fp8_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t
  * 1.5e-5 of the result's norm on normal data).
  *   a          M lines of length K, scales MX_FP8_LINE
  *   b          N lines of length K, scales of b_kind
- *   M, N, K    any; M or N 0: nothing to do, K <= 0 is rejected
+ *   M, N, K    M or N 0: nothing to do, K <= 0 is rejected; fewer than 2^23
+ *              tiles of 128 x 128 in C, and N < 2^27
  *   c, ldc     device, row-major [M][ldc], fp32 or bf16 (round to nearest even
  *              of the fp32 result), aligned to its element size, ldc >= N;
  *              must not overlap an operand
@@ -455,7 +456,7 @@ int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out);
  *   gets s = NaN and codes 0.
  * w and copy come from the moments before that cast.
  *   tensors    host array of count entries, read before the call returns; any
- *              count (one launch for each 48); n = 0 entries are skipped; the
+ *              count (one launch for each 48); n = 0 entries are skipped, n < 2^36; the
  *              arrays of all entries must not overlap, and each is aligned to
  *              its element (w, m, v, g, copy 16-byte aligned, 8-bit m and v
  *              8-byte aligned: fastest)

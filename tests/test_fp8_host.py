@@ -262,3 +262,13 @@ def test_operands_of_one_line_and_none():
             q = empty_fp8(lines, k, "cpu", kind=kind)
             q.check("q")
             assert q.c_struct().ld_codes >= q.codes.shape[1] and api._fp8_blocks(k) * 128 == q.codes.shape[1]
+
+
+def test_sizes_past_a_launch_are_refused():
+    """A grid holds fewer than 2^32 threads: what would need more is an invalid argument, not a device error."""
+    thin = f8(lds=1 << 31)
+    assert quant(rows=1 << 30, cols=8, ld=8, rq=thin, cq=f8(ld=1 << 30)) == 1
+    assert gemm(M=1, N=1 << 27, a=thin, b=thin, ldc=1 << 27) == 1
+    assert gemm(M=1 << 30, N=1, a=thin, b=thin) == 1
+    assert gemm(M=1 << 16, N=1 << 21, a=thin, b=thin, ldc=1 << 21) == 1
+    assert step(tensor=dict(n=1 << 36)) == 1

@@ -416,6 +416,9 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
     if axis != "row":
         q = col_out if col_out is not None else empty_fp8(cols, rows, dev, fmt, kind)
         out["col"], c[1] = q, _fp8_output(q, col_out is not None, "col_out", cols, rows, fmt, kind, dev)
+    if axis == "both" and row_out is not None and col_out is not None and x.numel():
+        if c[0].codes == c[1].codes or c[0].scales == c[1].scales:
+            raise ValueError("row_out and col_out share memory")
     _launch(x.get_device(), "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _FP8_FMT[fmt],
             _FP8_KIND[kind], _lib.AXIS[axis], *c)
     return out
@@ -490,7 +493,7 @@ class AdamWTensors:
     """The tensors that adamw_step updates, checked and laid out once: float32 master weights, their gradients
     (float32 or bf16), their states (all of 8 or all of 32 bits) and, if given, the bf16 copies that a step writes.
 
-    Every tensor is contiguous, and none may be given twice.  The object holds the tensors themselves; one whose
+    Every tensor is contiguous, and no two that a step writes may share memory.  The object holds the tensors themselves; one whose
     storage is replaced (Tensor.data, resize_) needs a new object, and new gradient tensors go in by set_grads.
     """
 
@@ -502,7 +505,7 @@ class AdamWTensors:
         self.device = self.params[0].device if self.params else None
         self.bits = self.states[0].bits if self.states else 32
         self._c = (_lib.AdamwTensorC * max(1, len(self.params)))()
-        starts = set()
+        spans = []                # (first byte, byte past the last, tensor) of everything a step writes
         for i, (w, s, h) in enumerate(zip(self.params, self.states, self.copies)):
             self._hold(i, "weight", w, torch.float32, w.numel())
             if s.bits != self.bits:
@@ -516,16 +519,18 @@ class AdamWTensors:
                 each.append(("copy", h, torch.bfloat16, w.numel()))
             for name, x, dtype, n in each:
                 self._hold(i, name, x, dtype, n)
-            if w.numel():
-                mine = [w.data_ptr()] + [x.data_ptr() for _, x, _, _ in each]
-                if len(set(mine)) < len(mine) or not starts.isdisjoint(mine):
-                    raise ValueError("tensor %d: a weight, state or copy is given twice" % i)
-                starts.update(mine)
+            for x in [w] + [x for _, x, _, _ in each]:
+                if x.numel():
+                    spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i))
             c = self._c[i]
             c.w, c.m, c.v, c.n = w.data_ptr(), s.m.data_ptr(), s.v.data_ptr(), w.numel()
             if self.bits == 8:
                 c.m_scales, c.v_scales = s.m_scale.data_ptr(), s.v_scale.data_ptr()
             c.copy = h.data_ptr() if h is not None else None
+        spans.sort()
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("tensors %d and %d: a weight, state or copy overlaps another" % (i, j))
         self.set_grads(grads)
 
     def _hold(self, i, name, x, dtype, n):

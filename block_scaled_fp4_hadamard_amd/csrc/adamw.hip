@@ -42,7 +42,7 @@ namespace {
 constexpr int kAwThreads = 512;
 constexpr int kAwChunk = 8 * kAwThreads;
 constexpr unsigned kAwGrid = 1024;         // 4 workgroups on each of the 256 CUs
-constexpr unsigned kAwMost = 1u << 22;     // a grid holds fewer than 2^32 threads; the workgroups take more chunks in turn
+constexpr unsigned kAwMost = 1u << 22;     // a grid holds fewer than 2^32 threads; further chunks are taken in turn
 
 struct AdamwArgs {
   AdamwTensor t[kAdamwGroup];

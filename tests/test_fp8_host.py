@@ -272,3 +272,26 @@ def test_sizes_past_a_launch_are_refused():
     assert gemm(M=1 << 30, N=1, a=thin, b=thin) == 1
     assert gemm(M=1 << 16, N=1 << 21, a=thin, b=thin, ldc=1 << 21) == 1
     assert step(tensor=dict(n=1 << 36)) == 1
+
+
+def test_shared_memory_is_refused():
+    """Operands that a call writes twice: one output for both axes, weights, states or copies that overlap in part."""
+    x, q = torch.zeros((128, 128), dtype=torch.bfloat16), empty_fp8(128, 128, "cpu")
+    other = empty_fp8(128, 128, "cpu")
+    for col in (q, Fp8Tensor(other.codes, q.scales, 128), Fp8Tensor(q.codes, other.scales, 128)):
+        with pytest.raises(ValueError, match="share memory"):
+            fp8_quantize(x, axis="both", row_out=q, col_out=col)
+    none = [empty_fp8(0, 8, "cpu"), empty_fp8(8, 0, "cpu")]        # nothing is written: only the host tensor is refused
+    with pytest.raises(ValueError, match="CUDA"):
+        fp8_quantize(torch.zeros((0, 8), dtype=torch.bfloat16), axis="both", row_out=none[0], col_out=none[1])
+    flat, moments = torch.zeros(1000), torch.zeros(4000)
+    m = [moments[1000 * i:1000 * i + 500] for i in range(4)]
+    g = torch.zeros(500)
+    ok = [AdamWState(m[0], m[1]), AdamWState(m[2], m[3])]
+    AdamWTensors([flat[:500], flat[500:]], [g, g], ok)            # one gradient for both is read only
+    half = torch.zeros(600, dtype=torch.bfloat16)
+    for bad in (dict(params=[flat[:500], flat[499:999]]), dict(states=[AdamWState(moments[:500], moments[100:600]), ok[1]]),
+                dict(states=[ok[0], AdamWState(flat[:500], m[3])]), dict(copies=[half[:500], half[100:]]),
+                dict(copies=[half[:500], flat[:250].view(torch.bfloat16)])):
+        with pytest.raises(ValueError, match="overlaps"):
+            AdamWTensors(**{**dict(params=[flat[:500], flat[500:]], grads=[g, g], states=ok), **bad})

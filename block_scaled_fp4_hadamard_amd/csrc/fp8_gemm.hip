@@ -225,21 +225,27 @@ __device__ __forceinline__ const T* uniform(const T* p) {
 
 // ---------------------------------------------------------------------------
 // Few rows of A (single tokens, short batches): the operand that matters is
-// B, read once from HBM.  A workgroup takes 16 J columns of C and all M <= 16 F
-// rows; its waves take the K blocks in turn, straight from memory to registers
-// with U blocks in flight, and their sums meet in LDS in the waves' order.
-// Rows past M and columns past N read the last one and are not stored.
+// B, read once from HBM.  A workgroup takes 16 J columns of C (few_columns) and
+// all M <= 16 F rows; its waves take the K blocks in turn, straight from memory
+// to registers with U blocks in flight, and their sums meet in LDS in the
+// waves' order.  Rows past M and columns past N read the last one and are not
+// stored.
 //
-// Memory-bound: one row takes 7.5 us with 6144 x 4096 (3.4 TB/s with the launch,
-// back to back in a graph), 12.7 us with 4096 x 14336 (4.6), 21.7 us with 28672 x
-// 4096 (5.4).  Eight waves rather than a split over workgroups: the whole of B
-// is in flight at once already, and no second launch joins the parts.
+// Memory-bound: one row takes 7.0 us with 6144 x 4096 (3.6 TB/s with the launch,
+// back to back in a graph), 11.1 us with 4096 x 14336 (5.3), 74 us with 28672 x
+// 14336 (5.6); sixteen rows 8.4, 15.5 and 80 us, 32 rows 10.7, 22 and 95.  Eight waves
+// rather than a split over workgroups: no second launch joins the parts.
+// Sixteen waves took the same or more.
 constexpr int kFewWaves = 8;
 
 template <int AF, int BF, int KIND, int OUT, int F, int J>
 __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams p) {
   constexpr bool kExact = OUT == MX_OUT_F32;
-  constexpr int U = F == 1 ? 4 : 2;
+  // Fewer loads in flight are faster where they suffice: a fragment's two 16-byte pieces of a row are two
+  // instructions' halves of one line, and with one block in flight a wave the second still finds it in the L1 (one row,
+  // 8192 x 14336: 18.9 us against 22.6 with four blocks).  Where few waves are resident, or the widening and the second
+  // A fragment hold up the next loads, more are.
+  constexpr int U = F == 2 ? (kExact ? (J == 3 ? 1 : 2) : (J <= 2 ? 1 : 2)) : kExact && J >= 3 ? 4 : 1;
   __shared__ __attribute__((aligned(16))) v4f part[kFewWaves][F * J][64];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int lrow = lane & 15, q = lane >> 4;
@@ -949,6 +955,35 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t 
   return plan;
 }
 
+// Column fragments of a workgroup in the kernel for few rows.  Every 256 workgroups are a round of the chip, and a
+// round's time goes by the operand rows that its workgroups read, B's and A's: with K 14336 (bf16 output) 10, 17, 23
+// and 29 us for 1 to 4 fragments and one row of A, 21, 29, 38 and 44 with 32 rows.  No choice reads B faster than HBM
+// gives it.  fp32 output takes longer with 3 and 4 fragments, whose widened codes leave room for half the waves.  In
+// units of 7 us there: 32 x 6144 x 14336 took 41 us in two rounds of one fragment and 29 in one of two, 16 x 28672 x
+// 14336 104, 90, 90 and 80 with 1 to 4 fragments, 98, 92, 118 and 107 to fp32.
+int few_columns(int64_t M, int64_t N, bool exact) {
+  const double slower[2][4] = {{1.0, 1.0, 1.3, 1.4}, {1.0, 1.0, 0.93, 1.07}};      // fp32: up to 16 rows, and above
+  int best = 1;
+  double least = 0.0;
+  for (int j = 1; j <= 4; ++j) {
+    const int64_t groups = (N + 16 * j - 1) / (16 * j), rounds = (groups + 255) / 256;
+    const double round = (j + 0.5 + 0.05 * (double)(M - 1)) * (exact ? slower[M > 16][j - 1] : 1.0);
+    const double cost = (double)rounds * round, read = 1.4 * (double)N / 4096;
+    const double units = cost > read ? cost : read;
+    if (j == 1 || units < least) {
+      best = j;
+      least = units;
+    }
+  }
+  return best;
+}
+
+template <int AF, int BF, int KIND, int OUT, int F, int J>
+void few(const Fp8GemmParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, J>), dim3((unsigned)((p.N + 16 * J - 1) / (16 * J))),
+                     dim3(64 * kFewWaves), 0, s, p);
+}
+
 template <int AF, int BF, int KIND, int OUT, int F>
 void launch_few(const Fp8GemmParams& p, hipStream_t s) {
   for (int64_t m = 0; m < p.M; m += 16 * F) {
@@ -957,13 +992,12 @@ void launch_few(const Fp8GemmParams& p, hipStream_t s) {
     r.a_scales += m;
     r.M = p.M - m < 16 * F ? p.M - m : 16 * F;
     r.c = (uint8_t*)p.c + m * p.ldc * (OUT == MX_OUT_F32 ? 4 : 2);
-    // two column fragments a workgroup where that leaves one for every CU
-    if (p.N >= 32 * 256)
-      hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, 2>), dim3((unsigned)((p.N + 31) / 32)),
-                         dim3(64 * kFewWaves), 0, s, r);
-    else
-      hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, 1>), dim3((unsigned)((p.N + 15) / 16)),
-                         dim3(64 * kFewWaves), 0, s, r);
+    switch (few_columns(r.M, p.N, OUT == MX_OUT_F32)) {
+      case 1: few<AF, BF, KIND, OUT, F, 1>(r, s); break;
+      case 2: few<AF, BF, KIND, OUT, F, 2>(r, s); break;
+      case 3: few<AF, BF, KIND, OUT, F, 3>(r, s); break;
+      default: few<AF, BF, KIND, OUT, F, 4>(r, s);
+    }
   }
 }
 

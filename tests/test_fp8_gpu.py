@@ -378,3 +378,21 @@ def test_infinities_stay_infinite(M, N, K, kind, bf16):
     if M > 3:
         rest = tuple(np.ascontiguousarray(x) for x in (clean[0][3:], clean[1][:, 3:]))
         assert_product(got[3:], rest, "e5m2", (bc, bsc), "e4m3", kind, bf16, "rest")
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["line", "tile"])
+@pytest.mark.parametrize("M", [1, 16, 17, 32])
+@pytest.mark.parametrize("N", [4095, 5001, 10241, 14335, 20490, 28673])
+def test_few_rows_over_all_widths(M, N, kind, bf16):
+    """Every number of column fragments that the kernel for few rows takes, with a part-filled last one."""
+    K = 300 + 1100 * (N % 2)
+    rng = np.random.default_rng(M * N)
+    a, qa = operand(M, K, "line", "e4m3", rng)
+    b, qb = operand(N, K, kind, "e5m2", rng)
+    announce("fp8 few %dx%dx%d %s %s" % (M, N, K, kind, "bf16" if bf16 else "fp32"))
+    buf = torch.full((M + 1, N + 5), 7.0, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    got = fp8_gemm(qa, qb, out=buf[:M, :N])
+    torch.cuda.synchronize()
+    assert_product(got, a, "e4m3", b, "e5m2", kind, bf16, "few")
+    assert bool((buf[M] == 7.0).all()) and bool((buf[:, N:] == 7.0).all())

@@ -930,10 +930,11 @@ int best_splits(int64_t tiles, int64_t nk, double outputs, bool exact) {
   return best;
 }
 
-// By measurement (bf16 output, tile scales): up to 32 rows of A, reading B once wins (16 x 6144 x 4096: 10 us
-// against 16; 64 rows: 22 against 16).  Above, a K block of a full round of the chip costs about 1.67 us in 256 x 256
-// tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU, half the work; about 0.7 us with one a CU), and the fewest
-// such times win.  fp32 output always takes the small tiles, whose wave leaves room for the widened operands.
+// By measurement (bf16 output, tile scales): up to 32 rows of A, reading B once wins (16 x 6144 x 4096: 8.4 us against
+// 16; 64 rows, as four row fragments, took 22 against 16).  Above, a K block of a full round of the chip costs about
+// 1.67 us in 256 x 256 tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU, half the work; about 0.7 us with one a
+// CU), and the fewest such times win.  fp32 output always takes the small tiles, whose wave leaves room for the widened
+// operands.
 Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lda_scales, int64_t ldb_scales,
              int out_kind) {
   Plan plan{Path::kFew, 1, {}};

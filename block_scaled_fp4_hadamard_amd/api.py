@@ -569,8 +569,9 @@ def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
 
     step counts from 1.  lr and step are numbers, or one-element CUDA tensors (float32, int64) that the kernel reads,
     so that a captured graph replays with values that move on.  rounding and seed are those of 8-bit states: "rtne", or
-    "sr" with another seed for each step.  grad_scale: a one-element float32 CUDA tensor that every gradient is
-    multiplied by first (clipping, loss scaling).
+    "sr" with another seed for each step; a step on the device is added to the seed, so that every replay of a graph
+    draws anew.  grad_scale: a one-element float32 CUDA tensor that every gradient is multiplied by first (clipping,
+    loss scaling).
     """
     if rounding not in _lib.ROUND:
         raise ValueError("unknown rounding %r" % (rounding,))

@@ -141,9 +141,13 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint64_t group, ui
 template <int BITS, int ROUND>
 __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const AdamwArgs a) {
   AdamwCoef c = a.coef;
-  if (a.step.step_dev != nullptr || a.step.lr_dev != nullptr)
-    c = coefficients(a.step, a.step.lr_dev ? (double)*a.step.lr_dev : a.step.lr,
-                     a.step.step_dev ? *a.step.step_dev : a.step.step);
+  uint64_t seed = a.step.seed;
+  if (a.step.step_dev != nullptr || a.step.lr_dev != nullptr) {
+    const int64_t step = a.step.step_dev ? *a.step.step_dev : a.step.step;
+    c = coefficients(a.step, a.step.lr_dev ? (double)*a.step.lr_dev : a.step.lr, step);
+    // the seed is fixed when a graph is captured: the device's step gives every replay draws of its own
+    if (a.step.step_dev != nullptr) seed += (uint64_t)step;
+  }
   const bool scaled = a.step.grad_scale != nullptr;
   const float gs = scaled ? *a.step.grad_scale : 1.0f;
   const uint32_t chunks = a.end[a.count - 1];
@@ -226,8 +230,8 @@ __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const AdamwArgs a) {
     if constexpr (BITS == 8) {
       const uint64_t group = (uint64_t)at >> 3;
       const uint32_t stream = 4u + 2u * (uint32_t)(a.first + ti);
-      mc = encode8<true, ROUND>(m, group, stream, a.step.seed, sm);
-      vc = encode8<false, ROUND>(v, group, stream + 1u, a.step.seed, sv);
+      mc = encode8<true, ROUND>(m, group, stream, seed, sm);
+      vc = encode8<false, ROUND>(v, group, stream + 1u, seed, sv);
       if (cnt > 0 && (threadIdx.x & 15) == 0) {
         t.m_scales[at >> 7] = sm;
         t.v_scales[at >> 7] = sv;

@@ -463,11 +463,14 @@ int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out);
  *   eps        >= 0; with eps 0 an element whose moments are both 0 becomes NaN
  *   step       t >= 1; if step_dev is not NULL the device's int64 is read
  *              instead when the kernel runs (it must be >= 1), so that a
- *              captured graph can be replayed with a step that moves on
+ *              captured graph can be replayed with a step that moves on; the
+ *              draws of MX_ROUND_SR then take the key seed + that step (mod 2^64)
  *   lr         likewise, or the float32 at lr_dev
  *   grad_scale NULL, or a device float32 (the clipping or loss-scale factor)
  *   round      how 8-bit moments are cast (no meaning with bits 32)
- *   seed       keys the draws of MX_ROUND_SR; pass another one each step
+ *   seed       keys the draws of MX_ROUND_SR; pass another one each step, or
+ *              step_dev (a captured call with a host step repeats its draws at
+ *              every replay, as it repeats its step)
  */
 typedef struct {
   float *w;

@@ -233,3 +233,62 @@ def test_linear_layer_training_steps():
         assert_bytes_equal(master.cpu().numpy().reshape(-1).view(np.uint32), host[0][0].view(np.uint32), "master")
         assert_bytes_equal(copy.view(torch.int16).cpu().numpy().view(np.uint16), synth.f32_to_bf16_bits(host[0][0]).reshape(O, I), "copy")
         assert_bytes_equal(opt.states[0].v.cpu().numpy().reshape(-1), host[0][1][2], "v codes")
+
+
+def test_stochastic_rounding_draws_anew_at_every_replay():
+    """A captured 8-bit step with its step on the device: replay t takes the draws of key seed + t, which are those of an
+    eager call with that seed, so that a moment whose gradients stand still keeps moving.  Eager work between replays."""
+    rng = np.random.default_rng(18)
+    sizes = (1000, 5, 4097)
+    host = draw(sizes, 8, rng)
+    gs = [gradient(n, rng, False) for n in sizes]
+    tensors = AdamWTensors([cuda(h[0]) for h in host], grads_of(gs, False), [state_of(h[1], 8) for h in host])
+    eager = AdamWTensors([cuda(h[0]) for h in host], grads_of(gs, False), [state_of(h[1], 8) for h in host])
+    step = torch.tensor([6], dtype=torch.int64, device="cuda")
+    seed = 2 ** 64 - 9                      # the key passes 2^64 within the replays
+    announce("adamw sr graph")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        adamw_step(tensors, step=step, rounding="sr", seed=seed, **HYPER)
+    for t in range(6, 11):
+        g.replay()
+        torch.cuda.synchronize()
+        oracle_step(host, gs, 8, adamw.coefficients(step=t, **HYPER), None, (seed + t) % 2 ** 64)
+        compare(tensors, host, 8, "replay %d" % t)
+        adamw_step(eager, step=t, rounding="sr", seed=(seed + t) % 2 ** 64, **HYPER)
+        compare(eager, host, 8, "eager %d" % t)
+        step += 1
+
+
+def test_second_moment_moves_in_a_graph():
+    """1 - beta2 of 2^-12 moves v by less than half a code step of 2^-4 at each step: round-to-nearest would keep every
+    code, and so would draws that repeat.  v starts at 1/4 of g^2; after n steps its exact value is g^2 (1 - 3/4 beta2^n),
+    and the mean over the elements follows it: one step's rounding is unbiased (16-bit draws: to 2^-16 of a step) and off
+    by less than a code step, at most 2^-3 of v <= g^2, so the mean of N elements after n steps is within
+    6 sqrt(n / N) 2^-3 / 2 (six standard deviations, each draw's at most half a step) + n 2^-19 of g^2, and float32 adds
+    four roundings a step, n 2^-22."""
+    N, n, beta2 = 128 * 512, 400, 1.0 - 2.0 ** -12
+    w, g = torch.zeros(N, device="cuda"), torch.full((N,), 1e-3, device="cuda")
+    # the last of each block sets the scale: its gradient is twice the others', its v the square of it all along
+    g[127::128] = 2e-3
+    v = (g * g).cpu().numpy() * np.where(np.arange(N) % 128 == 127, 1.0, 0.25).astype(np.float32)
+    vc, vs = adamw.encode_state(v, False)
+    start = adamw.decode_state(vc, vs, False)
+    state = AdamWState(torch.zeros(N, dtype=torch.uint8, device="cuda"), cuda(vc), torch.zeros(N // 128, device="cuda"), cuda(vs))
+    tensors = AdamWTensors([w], [g], [state])
+    step = torch.ones(1, dtype=torch.int64, device="cuda")
+    announce("adamw sr drift")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        adamw_step(tensors, lr=0.0, step=step, beta2=beta2, rounding="sr", seed=3)
+        step += 1
+    for _ in range(n):
+        graph.replay()
+    torch.cuda.synchronize()
+    got = adamw.decode_state(state.v.cpu().numpy(), state.v_scale.cpu().numpy(), False).astype(np.float64)
+    small = np.arange(N) % 128 != 127
+    gg = float(np.float32(1e-3)) ** 2
+    want = gg + (start[small].astype(np.float64).mean() - gg) * beta2 ** n
+    bound = (6 * np.sqrt(n / small.sum()) * 2.0 ** -4 + n * 2.0 ** -19 + n * 2.0 ** -22) * gg
+    print("mean v / g^2: %.5f, exact %.5f, bound %.5f" % (got[small].mean() / gg, want / gg, bound / gg))
+    assert abs(got[small].mean() - want) <= bound

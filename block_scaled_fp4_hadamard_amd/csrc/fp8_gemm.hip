@@ -30,12 +30,13 @@
 // 16 h + 4 j + i (h = 0..3, i = 0..3) as its rows 4 h + i: over j = 0..3 a lane
 // then ends with the sixteen consecutive columns 16 (l / 16) .. + 15 of its row.
 //
-// Three kernels: few rows of A, 128 x 128 tiles, 256 x 256 tiles (plan_of says
+// Three kernels: few rows of A, 128 x 128 tiles, 256 x 256 tiles (fp8_plan says
 // which product runs where).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <utility>
 #include "fp8_kernels.h"
+#include "fp8_path.h"
 
 namespace mx {
 
@@ -44,8 +45,6 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kKB = 128;      // bytes (values) of a row per K step
 
 // 16-byte piece position in a 128-byte LDS row.  A 16-byte LDS read serves the
 // wave in four groups of 16 lanes, taken from neighbouring 16-lane rows: 0-3,
@@ -201,8 +200,6 @@ __device__ __forceinline__ void store_rows(const Fp8GemmParams& p, int64_t m0, i
   }
 }
 
-constexpr int kXcds = 8;
-
 // Global -> LDS copy of 16 (4) bytes per lane: LDS address = M0 + size * lane.  Inline asm, so that the
 // compiler places no waits of its own for it; it writes no register.  An SALU write of M0 needs one wait
 // state before the copy reads it.
@@ -225,7 +222,7 @@ __device__ __forceinline__ const T* uniform(const T* p) {
 
 // ---------------------------------------------------------------------------
 // Few rows of A (single tokens, short batches): the operand that matters is
-// B, read once from HBM.  A workgroup takes 16 J columns of C (few_columns) and
+// B, read once from HBM.  A workgroup takes 16 J columns of C (fp8_few_columns) and
 // all M <= 16 F rows; its waves take the K blocks in turn, straight from memory
 // to registers with U blocks in flight, and their sums meet in LDS in the
 // waves' order.  Rows past M and columns past N read the last one and are not
@@ -368,7 +365,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams
 // 4096 x 14336 x 8001 with line scales takes 818 us (1150 TFLOP/s; a bf16 product
 // of the library 1445): the widening and the joins issue 280 vector instructions
 // beside 64 matrix instructions, and the chip runs them at 1.6 GHz.
-constexpr int kMT = 128, kMThreads = 256, kMStage = kMT * kKB;
+constexpr int kMThreads = 256, kMStage = kMT * kKB;
 
 struct MidMap {
   int tiles_m, tiles_n, splits, total, per_xcd;    // total = tiles_m * tiles_n * splits
@@ -649,15 +646,8 @@ __global__ void __launch_bounds__(256) fp8_mm_sum(const Fp8GemmParams p, const f
 // operations an element; the library's product with one scale for each whole
 // operand reaches 2680 to 3100.  The matrix cores are busy 65% of the cycles, and the
 // chip lowers its clock to 1.8 GHz for it.
-constexpr int kBT = 256, kBThreads = 512, kGroup = 32;
+constexpr int kBThreads = 512;
 constexpr int kStage = kBT * kKB;
-
-// Tiles are dealt in groups of 4 (M) x 8 (N) to the 8 XCDs, a group to the 32 CUs of one, so that the tiles
-// an XCD computes at once share 4 A strips and 8 B strips in its L2; 2 x 16 or 1 x 32 where there are fewer than
-// four rows of tiles.
-struct BigMap {
-  int tiles_m, tiles_n, group_m, groups_m, groups, rounds;
-};
 
 __device__ __forceinline__ int next_tile(const BigMap& t, int r, int& bm, int& bn) {
   const int xcd = blockIdx.x % kXcds, member = blockIdx.x / kXcds;
@@ -886,99 +876,6 @@ __global__ void __launch_bounds__(kBThreads, 2) fp8_mm_big(const Fp8GemmParams p
   }
 }
 
-// How a product runs.  The copies of the two tiled kernels address a tile's rows by 32-bit offsets whose row pitch
-// is a 24-bit factor; operands with longer rows run on the kernel for few rows, 32 rows of A at a time.
-enum class Path { kFew, kMid, kBig };
-
-struct Plan {
-  Path path;
-  int splits;
-  BigMap big;
-};
-
-BigMap big_map(int64_t M, int64_t N) {
-  BigMap map;
-  map.tiles_m = (int)((M + kBT - 1) / kBT);
-  map.tiles_n = (int)((N + kBT - 1) / kBT);
-  map.group_m = map.tiles_m >= 3 ? 4 : map.tiles_m;
-  map.groups_m = (map.tiles_m + map.group_m - 1) / map.group_m;
-  const int group_n = kGroup / map.group_m;
-  map.groups = map.groups_m * ((map.tiles_n + group_n - 1) / group_n);
-  map.rounds = (map.groups + kXcds - 1) / kXcds;
-  return map;
-}
-
-// Into how many parts the K blocks of at most 256 small tiles are split: the least time by what was measured (us).  A
-// K block takes 0.55 to 0.68 (fp32 output: 1.0) while every CU has one workgroup at most, 0.8 to 0.9 (1.6) with two;
-// the parts' float32 sums cost 0.45 a megabyte, written and read back, and the second launch 4.5.  1000 x 2000 x 2048:
-// 14 us whole, 20 in two parts; 400 x 2000 x 8192: 44 whole, 23 in four; 333 x 4096 x 14336: 70 whole, 37 in five.
-int best_splits(int64_t tiles, int64_t nk, double outputs, bool exact) {
-  int best = 1;
-  double least = 0.0;
-  for (const int splits : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64}) {
-    const int64_t all = tiles * splits;
-    if (splits > 1 && (all > 512 || splits * 2 > nk)) break;
-    const double block = exact ? (all <= 256 ? 1.0 : 1.6)
-                               : (all <= 256 ? 0.55 + 0.13 * (double)all / 256 : 0.7 + 0.1 * (double)all / 256);
-    const double us = block * (double)((nk + splits - 1) / splits) +
-                      (splits > 1 ? 4.5 + 0.45e-6 * 4.0 * outputs * splits : 0.0);
-    if (splits == 1 || us < least) {
-      best = splits;
-      least = us;
-    }
-  }
-  return best;
-}
-
-// By measurement (bf16 output, tile scales): up to 32 rows of A, reading B once wins (16 x 6144 x 4096: 8.4 us against
-// 16; 64 rows, as four row fragments, took 22 against 16).  Above, a K block of a full round of the chip costs about
-// 1.67 us in 256 x 256 tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU, half the work; about 0.7 us with one a
-// CU), and the fewest such times win.  fp32 output always takes the small tiles, whose wave leaves room for the widened
-// operands.
-Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lda_scales, int64_t ldb_scales,
-             int out_kind) {
-  Plan plan{Path::kFew, 1, {}};
-  const int64_t lim = int64_t(1) << 24;
-  if (M <= 32 || lda >= lim || ldb >= lim || lda_scales >= lim || ldb_scales >= lim) return plan;
-  const int64_t nk = (K + kKB - 1) / kKB;
-  const int64_t tiles = ((M + kMT - 1) / kMT) * ((N + kMT - 1) / kMT);
-  plan.path = Path::kMid;
-  if (tiles <= 256) {
-    plan.splits = best_splits(tiles, nk, (double)M * (double)N, out_kind == MX_OUT_F32);
-    return plan;
-  }
-  if (out_kind == MX_OUT_BF16) {
-    plan.big = big_map(M, N);
-    const double rest = (double)(tiles % 512);
-    const double mid = 1.15 * (double)(tiles / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.7 : 1.15);
-    if (1.67 * plan.big.rounds < mid) plan.path = Path::kBig;
-  }
-  return plan;
-}
-
-// Column fragments of a workgroup in the kernel for few rows.  Every 256 workgroups are a round of the chip, and a
-// round's time goes by the operand rows that its workgroups read, B's and A's: with K 14336 (bf16 output) 10, 17, 23
-// and 29 us for 1 to 4 fragments and one row of A, 21, 29, 38 and 44 with 32 rows.  No choice reads B faster than HBM
-// gives it.  fp32 output takes longer with 3 and 4 fragments, whose widened codes leave room for half the waves.  In
-// units of 7 us there: 32 x 6144 x 14336 took 41 us in two rounds of one fragment and 29 in one of two, 16 x 28672 x
-// 14336 104, 90, 90 and 80 with 1 to 4 fragments, 98, 92, 118 and 107 to fp32.
-int few_columns(int64_t M, int64_t N, bool exact) {
-  const double slower[2][4] = {{1.0, 1.0, 1.3, 1.4}, {1.0, 1.0, 0.93, 1.07}};      // fp32: up to 16 rows, and above
-  int best = 1;
-  double least = 0.0;
-  for (int j = 1; j <= 4; ++j) {
-    const int64_t groups = (N + 16 * j - 1) / (16 * j), rounds = (groups + 255) / 256;
-    const double round = (j + 0.5 + 0.05 * (double)(M - 1)) * (exact ? slower[M > 16][j - 1] : 1.0);
-    const double cost = (double)rounds * round, read = 1.4 * (double)N / 4096;
-    const double units = cost > read ? cost : read;
-    if (j == 1 || units < least) {
-      best = j;
-      least = units;
-    }
-  }
-  return best;
-}
-
 template <int AF, int BF, int KIND, int OUT, int F, int J>
 void few(const Fp8GemmParams& p, hipStream_t s) {
   hipLaunchKernelGGL((fp8_mm_few<AF, BF, KIND, OUT, F, J>), dim3((unsigned)((p.N + 16 * J - 1) / (16 * J))),
@@ -993,7 +890,7 @@ void launch_few(const Fp8GemmParams& p, hipStream_t s) {
     r.a_scales += m;
     r.M = p.M - m < 16 * F ? p.M - m : 16 * F;
     r.c = (uint8_t*)p.c + m * p.ldc * (OUT == MX_OUT_F32 ? 4 : 2);
-    switch (few_columns(r.M, p.N, OUT == MX_OUT_F32)) {
+    switch (fp8_few_columns(r.M, p.N, OUT == MX_OUT_F32)) {
       case 1: few<AF, BF, KIND, OUT, F, 1>(r, s); break;
       case 2: few<AF, BF, KIND, OUT, F, 2>(r, s); break;
       case 3: few<AF, BF, KIND, OUT, F, 3>(r, s); break;
@@ -1004,14 +901,14 @@ void launch_few(const Fp8GemmParams& p, hipStream_t s) {
 
 template <int AF, int BF, int KIND, int OUT>
 void launch(const Fp8GemmParams& p, float* parts, int64_t parts_bytes, hipStream_t s) {
-  Plan plan = plan_of(p.M, p.N, p.K, p.lda, p.ldb, p.lda_scales, p.ldb_scales, OUT);
-  if (plan.path == Path::kFew) {
+  Fp8Plan plan = fp8_plan(p.M, p.N, p.K, p.lda, p.ldb, KIND == MX_FP8_TILE ? p.ldb_scales : 0, OUT == MX_OUT_F32);
+  if (plan.path == Fp8Path::kFew) {
     if (p.M <= 16) launch_few<AF, BF, KIND, OUT, 1>(p, s);
     else launch_few<AF, BF, KIND, OUT, 2>(p, s);
     return;
   }
   if constexpr (OUT == MX_OUT_BF16) {
-    if (plan.path == Path::kBig) {
+    if (plan.path == Fp8Path::kBig) {
       hipLaunchKernelGGL((fp8_mm_big<AF, BF, KIND>), dim3(kXcds * kGroup), dim3(kBThreads), 0, s, p, plan.big);
       return;
     }
@@ -1050,7 +947,7 @@ void launch_kinds(const Fp8GemmParams& p, int b_kind, int out_kind, float* w, in
 int64_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, int out_kind) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   const int64_t k = ((K + kKB - 1) / kKB) * kKB;
-  const Plan plan = plan_of(M, N, K, k, k, 1, 1, out_kind);
+  const Fp8Plan plan = fp8_plan(M, N, K, k, k, 0, out_kind == MX_OUT_F32);
   return plan.splits > 1 ? 4 * plan.splits * M * N : 0;
 }
 

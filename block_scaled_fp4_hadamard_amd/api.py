@@ -330,6 +330,19 @@ def _pitch(stride, rows, cols, name):
     return ld if rows > 1 else cols
 
 
+def _meet(x, y):
+    """Whether two regions of memory share a byte, each (address, rows, bytes of a row, bytes between rows)."""
+    (p, rows_p, wide_p, pitch_p), (q, rows_q, wide_q, pitch_q) = x, y
+    if p + (rows_p - 1) * pitch_p + wide_p <= q or q + (rows_q - 1) * pitch_q + wide_q <= p:
+        return False
+    if not (rows_p and wide_p and rows_q and wide_q):
+        return False
+    # each row of x against the last row of y that starts before its end: views side by side in one buffer are apart
+    start, other = p + pitch_p * torch.arange(rows_p), q + pitch_q * torch.arange(rows_q)
+    last = torch.searchsorted(other, start + wide_p) - 1
+    return bool(((last >= 0) & (other[last.clamp_min(0)] + wide_q > start)).any())
+
+
 def _launch(at, name, entry, *args):
     """entry(*args, stream) on the current stream of CUDA device number `at`, as the current device; a number below 0,
     a host tensor's, is refused."""
@@ -416,12 +429,26 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
     if axis != "row":
         q = col_out if col_out is not None else empty_fp8(cols, rows, dev, fmt, kind)
         out["col"], c[1] = q, _fp8_output(q, col_out is not None, "col_out", cols, rows, fmt, kind, dev)
-    if axis == "both" and row_out is not None and col_out is not None and x.numel():
-        if c[0].codes == c[1].codes or c[0].scales == c[1].scales:
-            raise ValueError("row_out and col_out share memory")
+    if row_out is not None or col_out is not None:
+        given = [("x", (x.data_ptr(), rows, 2 * cols, 2 * ld))]
+        for name, q, s in (("row_out", row_out, c[0]), ("col_out", col_out, c[1])):
+            if q is None or s is None:
+                continue
+            for part in _regions(q, s):
+                for other, region in given:
+                    if _meet(part, region):
+                        raise ValueError("%s and %s share memory" % (other, name))
+                given.append((name, part))
     _launch(x.get_device(), "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _FP8_FMT[fmt],
             _FP8_KIND[kind], _lib.AXIS[axis], *c)
     return out
+
+
+def _regions(q, c):
+    """The memory of an operand's codes and of its scales, as _meet takes it."""
+    lines, width = q.codes.shape
+    rows, cols = q.scales.shape
+    return (c.codes or 0, lines, width, c.ld_codes), (c.scales or 0, rows, 4 * cols, 4 * c.ld_scales)
 
 
 def _fp8_output(q, given, name, lines, k, fmt, kind, dev):
@@ -446,7 +473,8 @@ def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
         raise ValueError("a must be scaled by lines, got kind %r" % a.kind)
     at = a.codes.get_device()
     M, N = a.codes.shape[0], b.codes.shape[0]
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = a.codes.new_empty((M, N), dtype=out_dtype)
     elif out.dim() != 2 or out.shape[0] != M or out.shape[1] != N:
         raise ValueError("out must be a row-major (%d, %d) view" % (M, N))
@@ -455,12 +483,20 @@ def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
         raise ValueError("the output must be float32 or bfloat16, got %s" % out.dtype)
     if b.codes.get_device() != at or out.get_device() != at:
         raise ValueError("a, b and out must be on one device")
+    ldc = _pitch(out.stride(), M, N, "out")
+    if not fresh:
+        size = out.element_size()
+        region = (out.data_ptr(), M, size * N, size * ldc)
+        for name, q, c in (("a", a, ca), ("b", b, cb)):
+            for part in _regions(q, c):
+                if _meet(region, part):
+                    raise ValueError("out and %s share memory" % name)
     lib = _lib.lib()
     # the workspace is this call's own: held until the launch, its memory then goes to later work of this stream only
     size = lib.mx_fp8_gemm_workspace(M, N, a.k, kind)
     space = a.codes.new_empty(size) if size else None
     _launch(at, "mx_fp8_gemm", lib.mx_fp8_gemm, ca, _FP8_FMT[a.fmt], cb, _FP8_FMT[b.fmt], _FP8_KIND[b.kind], M, N, a.k,
-            out.data_ptr(), _pitch(out.stride(), M, N, "out"), kind, space.data_ptr() if size else None, size)
+            out.data_ptr(), ldc, kind, space.data_ptr() if size else None, size)
     return out
 
 

@@ -295,3 +295,59 @@ def test_shared_memory_is_refused():
                 dict(copies=[half[:500], flat[:250].view(torch.bfloat16)])):
         with pytest.raises(ValueError, match="overlaps"):
             AdamWTensors(**{**dict(params=[flat[:500], flat[500:]], grads=[g, g], states=ok), **bad})
+
+
+def operand_at(buf, at, lines, k, kind="line", pitch=None, scales_at=None, scales=None):
+    """An operand whose codes lie in a byte buffer from `at`, and its scales in `scales` (bytes) from `scales_at`."""
+    kb = -(-k // 128)
+    pitch = pitch or kb * 128
+    codes = buf.as_strided((lines, kb * 128), (pitch, 1), at)
+    if scales is None:
+        return Fp8Tensor(codes, empty_fp8(lines, k, "cpu", kind=kind).scales, k, "e4m3", kind)
+    shape = (kb, lines) if kind == "line" else (-(-lines // 128), kb)
+    return Fp8Tensor(codes, scales.view(torch.float32).as_strided(shape, (shape[1], 1), scales_at // 4), k, "e4m3", kind)
+
+
+def test_cast_outputs_that_overlap_in_part_are_refused():
+    """Outputs that share some bytes with one another or with x; views side by side in one buffer share none and pass on
+    to the next check, which refuses a host tensor."""
+    buf = torch.zeros(1 << 17, dtype=torch.uint8)
+    x = torch.zeros((128, 128), dtype=torch.bfloat16)
+    size = 128 * 128
+    other = empty_fp8(128, 128, "cpu")
+    xb = buf[:2 * size].view(torch.bfloat16).view(128, 128)
+    for bad in (dict(row_out=operand_at(buf, 0, 128, 128), col_out=operand_at(buf, size - 16, 128, 128)),
+                dict(row_out=operand_at(buf, 0, 128, 128), col_out=operand_at(buf, 16, 128, 128, pitch=256)),
+                dict(row_out=operand_at(buf, 0, 128, 128, pitch=256), col_out=operand_at(buf, 256 * 127, 128, 128, pitch=272)),
+                dict(row_out=operand_at(buf, 0, 128, 128), col_out=operand_at(buf, size, 128, 128, scales_at=size - 4, scales=buf)),
+                dict(row_out=operand_at(buf, 0, 128, 128, scales_at=256, scales=buf), col_out=other),
+                dict(row_out=operand_at(buf, 0, 128, 128, scales_at=size, scales=buf), col_out=operand_at(buf, size + 16, 128, 128)),
+                dict(x=xb, row_out=operand_at(buf, 2 * size - 16, 128, 128)),
+                dict(x=xb, col_out=operand_at(buf, 2 * size, 128, 128, scales_at=512, scales=buf)),
+                dict(x=xb, axis="row", row_out=operand_at(buf, 16, 128, 128))):
+        with pytest.raises(ValueError, match="share memory"):
+            fp8_quantize(**{**dict(x=x, axis="both"), **bad})
+    for good in (dict(row_out=operand_at(buf, 0, 128, 128, pitch=256), col_out=operand_at(buf, 128, 128, 128, pitch=256)),
+                 dict(row_out=operand_at(buf, 0, 128, 128), col_out=operand_at(buf, size, 128, 128, scales_at=2 * size, scales=buf)),
+                 dict(x=xb, row_out=operand_at(buf, 2 * size, 128, 128), col_out=operand_at(buf, 3 * size, 128, 128)),
+                 dict(x=xb, axis="row", row_out=other, col_out=operand_at(buf, 0, 128, 128))):      # col_out is not written
+        with pytest.raises(ValueError, match="CUDA"):
+            fp8_quantize(**{**dict(x=x, axis="both"), **good})
+
+
+def test_products_over_their_operands_are_refused():
+    buf = torch.zeros(1 << 18, dtype=torch.uint8)
+    a, b = operand_at(buf, 0, 20, 128), operand_at(buf, 4096, 24, 128, "tile", scales_at=8192, scales=buf)
+
+    def out(at, dtype, pitch=24):
+        return buf.view(dtype).as_strided((20, 24), (pitch, 1), at // dtype.itemsize)
+    for c in (out(2560 - 4, torch.float32), out(2560 - 2, torch.bfloat16), out(4096 - 1920 + 4, torch.float32),
+              out(4096 + 3068, torch.float32), out(8192, torch.float32), out(8194 - 960, torch.bfloat16),
+              out(64, torch.bfloat16, 4000)):
+        with pytest.raises(ValueError, match="share memory"):
+            fp8_gemm(a, b, out=c)
+    # beside the operands: behind a, behind b, and between the rows of an operand of a wide pitch
+    wide = operand_at(buf, 16384, 20, 128, pitch=256)
+    for q, c in ((a, out(2560, torch.bfloat16)), (a, out(8196, torch.float32)), (wide, out(16384 + 128, torch.float32, 64))):
+        with pytest.raises(ValueError, match="CUDA"):
+            fp8_gemm(q, b, out=c)

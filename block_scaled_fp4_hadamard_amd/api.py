@@ -2,6 +2,7 @@
 the tensor's device and launch on torch's current stream.  No arithmetic of
 the method happens here.
 """
+from bisect import bisect_left
 from dataclasses import dataclass
 
 import torch
@@ -529,8 +530,9 @@ class AdamWTensors:
     """The tensors that adamw_step updates, checked and laid out once: float32 master weights, their gradients
     (float32 or bf16), their states (all of 8 or all of 32 bits) and, if given, the bf16 copies that a step writes.
 
-    Every tensor is contiguous, and no two that a step writes may share memory.  The object holds the tensors themselves; one whose
-    storage is replaced (Tensor.data, resize_) needs a new object, and new gradient tensors go in by set_grads.
+    Every tensor is contiguous, and none that a step writes may share memory with another or with a gradient.  The
+    object holds the tensors themselves; one whose storage is replaced (Tensor.data, resize_) needs a new object, and
+    new gradient tensors go in by set_grads.
     """
 
     def __init__(self, params, grads, states, copies=None):
@@ -567,6 +569,7 @@ class AdamWTensors:
         for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("tensors %d and %d: a weight, state or copy overlaps another" % (i, j))
+        self._starts, self._spans = [start for start, _, _ in spans], spans
         self.set_grads(grads)
 
     def _hold(self, i, name, x, dtype, n):
@@ -584,6 +587,10 @@ class AdamWTensors:
             if not isinstance(g, torch.Tensor) or g.dtype not in (torch.float32, torch.bfloat16):
                 raise ValueError("tensor %d: its gradient must be float32 or bfloat16" % i)
             self._hold(i, "gradient", g, g.dtype, w.numel())
+            start = g.data_ptr()
+            at = bisect_left(self._starts, start + g.numel() * g.element_size()) - 1
+            if at >= 0 and g.numel() and self._spans[at][1] > start:
+                raise ValueError("tensors %d and %d: a gradient overlaps a weight, state or copy" % (i, self._spans[at][2]))
         for i, g in enumerate(grads):
             self._c[i].g = g.data_ptr()
             self._c[i].grad = _lib.OUT["f32" if g.dtype == torch.float32 else "bf16"]

@@ -456,9 +456,11 @@ int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out);
  *   gets s = NaN and codes 0.
  * w and copy come from the moments before that cast.
  *   tensors    host array of count entries, read before the call returns; any
- *              count (one launch for each 48); n = 0 entries are skipped, n < 2^36; the
- *              arrays of all entries must not overlap, and each is aligned to
- *              its element (w, m, v, g, copy 16-byte aligned, 8-bit m and v
+ *              count (one launch for each 48); n = 0 entries are skipped,
+ *              n < 2^36; what the step writes (w, m, v, their scales, copy) must
+ *              overlap no other array of any entry (gradients may be shared)
+ *              nor the device's step, lr and grad_scale; each array is aligned
+ *              to its element (w, m, v, g, copy 16-byte aligned, 8-bit m and v
  *              8-byte aligned: fastest)
  *   eps        >= 0; with eps 0 an element whose moments are both 0 becomes NaN
  *   step       t >= 1; if step_dev is not NULL the device's int64 is read

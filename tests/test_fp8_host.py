@@ -351,3 +351,28 @@ def test_products_over_their_operands_are_refused():
     for q, c in ((a, out(2560, torch.bfloat16)), (a, out(8196, torch.float32)), (wide, out(16384 + 128, torch.float32, 64))):
         with pytest.raises(ValueError, match="CUDA"):
             fp8_gemm(q, b, out=c)
+
+
+def test_gradients_over_what_a_step_writes_are_refused():
+    """A gradient that shares some bytes with a weight, state or copy, of its own tensor or of another, when the list is
+    made and when other gradients go in; what they share among themselves is only read."""
+    flat, g = torch.zeros(8000), torch.zeros(500)
+    w, m = [flat[:500], flat[600:1100]], [flat[1000 * i:1000 * i + 500] for i in range(2, 6)]
+    ok = dict(params=w, grads=[g, g], states=[AdamWState(m[0], m[1]), AdamWState(m[2], m[3])],
+              copies=[flat[6000:6250].view(torch.bfloat16), None])
+    t = AdamWTensors(**ok)
+    beside = [flat[500:600], flat[1100:1600], flat[7000:7500]]
+    half = flat[:7400].view(torch.bfloat16)
+    for bad in (flat[:500], flat[499:999], flat[400:900], flat[101:601], flat[2499:2999], flat[5001:5501], flat[5751:6251],
+                half[998:1498], half[12499:12999], half[11600:12100]):
+        with pytest.raises(ValueError, match="overlaps"):
+            AdamWTensors(**{**ok, "grads": [g, bad]})
+        with pytest.raises(ValueError, match="overlaps"):
+            t.set_grads([bad, g])
+    t.set_grads([beside[1], beside[2]])
+    t.set_grads([half[1000:1200].expand(1, 200).reshape(-1).repeat(3)[:500], beside[2]])
+    t.set_grads([half[13000:13500], half[12500:13000]])
+    assert t.grads[0] is not g
+    with pytest.raises(ValueError):
+        t.set_grads([g, flat[:500]])
+    assert t._c[0].g == t.grads[0].data_ptr() and t._c[1].g == t.grads[1].data_ptr()      # a refused call changes nothing

@@ -531,19 +531,27 @@ class AdamWTensors:
     (float32 or bf16), their states (all of 8 or all of 32 bits) and, if given, the bf16 copies that a step writes.
 
     Every tensor is contiguous, and none that a step writes may share memory with another or with a gradient.  The
-    object holds the tensors themselves; one whose storage is replaced (Tensor.data, resize_) needs a new object, and
-    new gradient tensors go in by set_grads.
+    object holds the tensors it was given: params, grads, states and copies are read-only, a state's field replaced
+    later is not seen, and a tensor whose storage is replaced (Tensor.data, resize_) needs a new object.  New gradient
+    tensors go in by set_grads.
     """
+    params = property(lambda self: self._params)
+    grads = property(lambda self: self._grads)
+    states = property(lambda self: self._states)
+    copies = property(lambda self: self._copies)
+    bits = property(lambda self: self._bits)
+    device = property(lambda self: self._device)
 
     def __init__(self, params, grads, states, copies=None):
-        self.params, self.states = list(params), list(states)
-        self.copies = list(copies) if copies is not None else [None] * len(self.params)
+        self._params, self._states = tuple(params), tuple(states)
+        self._copies = tuple(copies) if copies is not None else (None,) * len(self.params)
         if not len(self.params) == len(self.states) == len(self.copies):
             raise ValueError("params, states and copies must have the same length")
-        self.device = self.params[0].device if self.params else None
-        self.bits = self.states[0].bits if self.states else 32
+        self._device = self.params[0].device if self.params else None
+        self._bits = self.states[0].bits if self.states else 32
         self._c = (_lib.AdamwTensorC * max(1, len(self.params)))()
-        spans = []                # (first byte, byte past the last, tensor) of everything a step writes
+        self._written = []        # every tensor a step writes, held here whatever becomes of the states' fields
+        spans = []                # (first byte, byte past the last, tensor) of each
         for i, (w, s, h) in enumerate(zip(self.params, self.states, self.copies)):
             self._hold(i, "weight", w, torch.float32, w.numel())
             if s.bits != self.bits:
@@ -558,6 +566,7 @@ class AdamWTensors:
             for name, x, dtype, n in each:
                 self._hold(i, name, x, dtype, n)
             for x in [w] + [x for _, x, _, _ in each]:
+                self._written.append(x)
                 if x.numel():
                     spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i))
             c = self._c[i]
@@ -580,7 +589,7 @@ class AdamWTensors:
 
     def set_grads(self, grads):
         """Other gradient tensors for the steps to come."""
-        grads = list(grads)
+        grads = tuple(grads)
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d weights" % (len(grads), len(self.params)))
         for i, (g, w) in enumerate(zip(grads, self.params)):
@@ -594,7 +603,7 @@ class AdamWTensors:
         for i, g in enumerate(grads):
             self._c[i].g = g.data_ptr()
             self._c[i].grad = _lib.OUT["f32" if g.dtype == torch.float32 else "bf16"]
-        self.grads = grads
+        self._grads = grads
 
 
 def _scalar(value, dtype, name, dev):

@@ -1,6 +1,8 @@
 """Host side of the 8-bit operands and the AdamW step: pins of their oracles, and what the entry points refuse (CPU only:
 no call here reaches a kernel)."""
+import gc
 import math
+import weakref
 from fractions import Fraction
 
 import numpy as np
@@ -376,3 +378,24 @@ def test_gradients_over_what_a_step_writes_are_refused():
     with pytest.raises(ValueError):
         t.set_grads([g, flat[:500]])
     assert t._c[0].g == t.grads[0].data_ptr() and t._c[1].g == t.grads[1].data_ptr()      # a refused call changes nothing
+
+
+def test_the_list_of_a_step_cannot_change_under_it():
+    """The C entry reads as many tensors as the list was made of, at the addresses they had: the lists cannot grow or be
+    replaced, and a state's tensor that its owner replaces lives on, since steps still write it."""
+    w, g = torch.zeros(300), torch.zeros(300)
+    s = AdamWState.zeros_like(w, 8)
+    t = AdamWTensors([w], [g], [s], copies=[torch.zeros(300, dtype=torch.bfloat16)])
+    for name in ("params", "grads", "states", "copies"):
+        with pytest.raises(AttributeError):
+            getattr(t, name).append(w)
+        with pytest.raises(AttributeError):
+            setattr(t, name, [w, w])
+    with pytest.raises(AttributeError):
+        t.bits = 32
+    old = [weakref.ref(x) for x in (s.m, s.v, s.m_scale, s.v_scale, g, w)]
+    s.m, s.v, s.m_scale, s.v_scale = (torch.zeros(1) for _ in range(4))
+    del g, w
+    gc.collect()
+    assert all(r() is not None for r in old)
+    assert (t._c[0].m, t._c[0].v_scales) == (old[0]().data_ptr(), old[3]().data_ptr())

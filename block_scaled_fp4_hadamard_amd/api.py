@@ -317,6 +317,8 @@ def _fp8_blocks(n):
     return -(-n // FP8_BLOCK)
 
 
+# told which of the caller's tensors a kernel wrote, autograd refuses a backward that would read the old values
+_written = torch.autograd.graph.increment_version
 _FP8_FMT, _FP8_KIND, _Fp8TensorC = _lib.FP8_FMT, _lib.FP8_KIND, _lib.Fp8TensorC
 _OUT_KINDS = {torch.float32: _lib.OUT["f32"], torch.bfloat16: _lib.OUT["bf16"]}
 
@@ -442,6 +444,9 @@ def fp8_quantize(x, axis="row", kind="line", fmt="e4m3", row_out=None, col_out=N
                 given.append((name, part))
     _launch(x.get_device(), "mx_fp8_quantize", _lib.lib().mx_fp8_quantize, x.data_ptr(), rows, cols, ld, _FP8_FMT[fmt],
             _FP8_KIND[kind], _lib.AXIS[axis], *c)
+    for q, s in ((row_out, c[0]), (col_out, c[1])):
+        if q is not None and s is not None:
+            _written((q.codes, q.scales))
     return out
 
 
@@ -498,6 +503,8 @@ def fp8_gemm(a, b, out_dtype=torch.float32, out=None):
     space = a.codes.new_empty(size) if size else None
     _launch(at, "mx_fp8_gemm", lib.mx_fp8_gemm, ca, _FP8_FMT[a.fmt], cb, _FP8_FMT[b.fmt], _FP8_KIND[b.kind], M, N, a.k,
             out.data_ptr(), ldc, kind, space.data_ptr() if size else None, size)
+    if not fresh:
+        _written(out)
     return out
 
 
@@ -641,3 +648,4 @@ def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
         _lib.check(_lib.mx_adamw_step(*args, None), "mx_adamw_step")       # an empty list: only the checks run
     else:
         _launch(dev.index if dev.type == "cuda" else -1, "mx_adamw_step", _lib.lib().mx_adamw_step, *args)
+        _written(tensors._written)

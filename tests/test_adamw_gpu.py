@@ -292,3 +292,34 @@ def test_second_moment_moves_in_a_graph():
     bound = (6 * np.sqrt(n / small.sum()) * 2.0 ** -4 + n * 2.0 ** -19 + n * 2.0 ** -22) * gg
     print("mean v / g^2: %.5f, exact %.5f, bound %.5f" % (got[small].mean() / gg, want / gg, bound / gg))
     assert abs(got[small].mean() - want) <= bound
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_autograd_notices_what_the_operators_write(bits):
+    """A backward whose forward saved a weight, a copy, a moment, or an output that a later call has written raises instead
+    of using the new values; tensors that the call only reads still give gradients."""
+    w = torch.nn.Parameter(torch.randn(256, 256, device="cuda"))
+    g, copy = torch.randn(256, 256, device="cuda"), torch.zeros(256, 256, dtype=torch.bfloat16, device="cuda")
+    state = AdamWState.zeros_like(w, bits)
+    other = torch.ones(256, 256, device="cuda", requires_grad=True)
+    tensors = AdamWTensors([w], [g], [state], copies=[copy])
+    held = [(other * w.detach()).sum(), (other * copy).sum(), (other * (state.m if bits == 32 else state.v_scale[0])).sum()]
+    read = (other * g).sum()
+    announce("adamw autograd %d" % bits)
+    adamw_step(tensors, lr=1e-3, step=1)
+    for y in held:
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+    read.backward()
+    assert torch.equal(other.grad, g)
+    q = fp8_quantize(copy, axis="both")
+    c = torch.zeros(256, 256, device="cuda")
+    held = [(other * c).sum(), (other * q["row"].scales[0]).sum(), (other * q["col"].scales[0]).sum()]
+    read = (other * copy).sum()
+    fp8_quantize(copy, axis="row", row_out=q["row"])
+    fp8_gemm(q["row"], q["row"], out=c)
+    for y in held[:2]:
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+    held[2].backward()                      # the column output was not written
+    read.backward()

@@ -233,8 +233,6 @@ __device__ __forceinline__ const T* uniform(const T* p) {
 // 14336 (5.6); sixteen rows 8.4, 15.5 and 80 us, 32 rows 10.7, 22 and 95.  Eight waves
 // rather than a split over workgroups: no second launch joins the parts.
 // Sixteen waves took the same or more.
-constexpr int kFewWaves = 8;
-
 template <int AF, int BF, int KIND, int OUT, int F, int J>
 __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams p) {
   constexpr bool kExact = OUT == MX_OUT_F32;

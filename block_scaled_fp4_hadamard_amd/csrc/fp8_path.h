@@ -9,6 +9,7 @@ namespace mx {
 
 constexpr int kKB = 128;            // bytes (values) of a row per K step
 constexpr int kXcds = 8;
+constexpr int kFewWaves = 8;        // waves of a workgroup of the kernel for few rows
 constexpr int kMT = 128;            // tile of the kernel for mid-sized products
 constexpr int kBT = 256;            // tile of the kernel for large ones
 constexpr int kGroup = 32;          // tiles of a group: one for each CU of an XCD
@@ -97,17 +98,19 @@ inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ld
 // and 29 us for 1 to 4 fragments and one row of A, 21, 29, 38 and 44 with 32 rows.  No choice reads B faster than HBM
 // gives it.  fp32 output takes longer with 3 and 4 fragments, whose widened codes leave room for half the waves.  In
 // units of 7 us there: 32 x 6144 x 14336 took 41 us in two rounds of one fragment and 29 in one of two, 16 x 28672 x
-// 14336 104, 90, 90 and 80 with 1 to 4 fragments, 98, 92, 118 and 107 to fp32.
+// 14336 104, 90, 90 and 80 with 1 to 4 fragments, 98, 92, 118 and 107 to fp32.  A grid holds fewer than 2^32 threads,
+// which one fragment would pass at N = 2^27 - 1; the ABI refuses N >= 2^27.
 inline int fp8_few_columns(int64_t M, int64_t N, bool exact) {
   const double slower[2][4] = {{1.0, 1.0, 1.3, 1.4}, {1.0, 1.0, 0.93, 1.07}};      // fp32: up to 16 rows, and above
-  int best = 1;
+  int best = 0;
   double least = 0.0;
   for (int j = 1; j <= 4; ++j) {
     const int64_t groups = (N + 16 * j - 1) / (16 * j), rounds = (groups + 255) / 256;
+    if (groups * 64 * kFewWaves >= (int64_t(1) << 32)) continue;
     const double round = (j + 0.5 + 0.05 * (double)(M - 1)) * (exact ? slower[M > 16][j - 1] : 1.0);
     const double cost = (double)rounds * round, read = 1.4 * (double)N / 4096;
     const double units = cost > read ? cost : read;
-    if (j == 1 || units < least) {
+    if (best == 0 || units < least) {
       best = j;
       least = units;
     }

@@ -472,7 +472,7 @@ mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_ten
   if (s != MX_OK) return s;
   const uintptr_t esize = out == MX_OUT_F32 ? 4u : 2u;
   if (c == nullptr || ((uintptr_t)c % esize) != 0 || ldc < N) return MX_ERR_INVALID;
-  // few rows: 512 threads for each 32 columns
+  // few rows: 512 threads for each 16 to 64 columns (fp8_few_columns keeps the grid below 2^32 threads)
   if (too_many_tiles(M, N) || N >= (int64_t(1) << 27)) return MX_ERR_INVALID;
   if (workspace_bytes < 0 || !aligned16(workspace)) return MX_ERR_INVALID;
   mx::Fp8GemmParams p{};

@@ -81,3 +81,11 @@ def test_shapes_of_the_gpu_tests_take_the_kernels_they_are_meant_for(plans):
         for at, width in parts:
             covered[at:at + width] = True
         assert covered.all() and all(g[:2] == ("mid", 1) for g in plans([case(m, w, k) for _, w in parts]))
+
+
+def test_the_grid_of_the_kernel_for_few_rows_fits_a_launch(plans):
+    """512 threads for each 16 columns and fragment, fewer than 2^32 in all, up to the widest product the ABI takes."""
+    cases = [case(M, N, 128, exact=exact) for M in (1, 2, 16, 17, 31, 32) for exact in (False, True)
+             for N in (1, 16, 17, 4096, 128256, (1 << 26) + 1, (1 << 27) - 17, (1 << 27) - 1)]
+    for c, (path, _, _, columns) in zip(cases, plans(cases)):
+        assert path == "few" and 1 <= columns <= 4 and -(-c[1] // (16 * columns)) * 512 < 1 << 32, c

@@ -943,7 +943,6 @@ void launch_kinds(const Fp8GemmParams& p, int b_kind, int out_kind, float* w, in
 }  // namespace
 
 int64_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, int out_kind) {
-  if (M <= 0 || N <= 0 || K <= 0) return 0;
   const int64_t k = ((K + kKB - 1) / kKB) * kKB;
   const Fp8Plan plan = fp8_plan(M, N, K, k, k, 0, out_kind == MX_OUT_F32);
   return plan.splits > 1 ? 4 * plan.splits * M * N : 0;

@@ -496,6 +496,8 @@ mx_status mx_fp8_gemm(const mx_fp8_tensor* a, mx_fp8_fmt a_fmt, const mx_fp8_ten
 
 int64_t mx_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, mx_out out) {
   if (out != MX_OUT_F32 && out != MX_OUT_BF16) return 0;
+  // sizes that mx_fp8_gemm refuses, or whose rows no memory holds
+  if (M <= 0 || N <= 0 || K <= 0 || too_many_tiles(M, N) || K >= (int64_t(1) << 62)) return 0;
   return mx::fp8_gemm_workspace(M, N, K, out);
 }
 

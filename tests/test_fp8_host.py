@@ -399,3 +399,13 @@ def test_the_list_of_a_step_cannot_change_under_it():
     gc.collect()
     assert all(r() is not None for r in old)
     assert (t._c[0].m, t._c[0].v_scales) == (old[0]().data_ptr(), old[3]().data_ptr())
+
+
+def test_workspace_of_any_size_asked_for():
+    """Sizes that the product refuses need none, however large: the counts do not wrap."""
+    assert _lib.mx_fp8_gemm_workspace(300, 500, 8192, 1) == 16 * 300 * 500 * 4
+    top = (1 << 63) - 1
+    for M, N, K in (((1 << 42) - 1, (1 << 36) - 1, 4096), (1 << 62, 1 << 62, 1 << 20), (top, top, top), (300, 500, top),
+                    (300, 500, (1 << 62) - 1), (-1, 500, 4096), (300, 0, 4096), (300, 500, 0)):
+        assert _lib.mx_fp8_gemm_workspace(M, N, K, 0) == _lib.mx_fp8_gemm_workspace(M, N, K, 1) == 0
+    assert _lib.mx_fp8_gemm_workspace(300, 500, 8192, 2) == 0

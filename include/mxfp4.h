@@ -400,13 +400,16 @@ mx_status mx_fp8_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t
 /*
  * mx_fp8_gemm: C[m][n] = sum_k A[m][k] * B[n][k] on the operands' values:
  * each block of 128 k summed on the matrix cores, its two scales multiplied in
- * float32 (a product of scales that overflows float32 gives Inf or NaN), the
- * blocks added in float32.  For fp32 output a block's products are
+ * float32, the blocks added in float32.  For fp32 output a block's products are
  * exact and its sum is float32, |err| <= (128 * 2^-23 + (K / 128 + 2) * 2^-24)
  * * sum |a b|.  For bf16 output the 8-bit matrix instruction sums them, twice as
  * fast: among each 8 neighbouring k it drops what lies below 2^-13 of the
  * largest product, |err| < 2^-10 * sum |a b| before the rounding to bf16 (about
- * 1.5e-5 of the result's norm on normal data).
+ * 1.5e-5 of the result's norm on normal data).  Both hold where the scales'
+ * products and the sums are normal float32 numbers: a product of two scales
+ * that overflows gives Inf or NaN, and one below 2^-126 is a multiple of 2^-149
+ * (0 below 2^-150), |err| up to 2^-150 * sum |codes' products| + (K / 128 + 9) *
+ * 2^-150 more.
  *   a          M lines of length K, scales MX_FP8_LINE
  *   b          N lines of length K, scales of b_kind
  *   M, N, K    M or N 0: nothing to do, K <= 0 is rejected; fewer than 2^23

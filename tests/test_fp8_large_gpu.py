@@ -7,7 +7,7 @@ import torch
 from block_scaled_fp4_hadamard_amd import Fp8Tensor, fp8_gemm, fp8_quantize
 from gpu_helpers import announce
 from oracle import fp8
-from test_fp8_gpu import assert_product, operand
+from test_fp8_gpu import assert_product, operand, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -213,3 +213,29 @@ def test_large_products_of_normal_data(kind, fmt):
     part = got[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()].double().cpu().numpy()
     assert np.all(np.abs(part - c) <= 2.0 ** -14 * g + 2.0 ** -8 * (np.abs(c) + 2.0 ** -14 * g))
     assert np.linalg.norm(part - c) <= 2.0 ** -8 / np.sqrt(3) * np.linalg.norm(c)
+
+
+# few rows, mid (whole and in parts), large
+SMALL_SCALES = [(3, 300, 1100), (20, 40, 700), (300, 300, 300), (200, 260, 4100), (4352, 2047, 300)]
+
+
+@pytest.mark.parametrize("low", [-134, -145, -155])
+@pytest.mark.parametrize("kind", ["line", "tile"])
+@pytest.mark.parametrize("m,n,k", SMALL_SCALES)
+def test_scales_whose_product_is_not_a_normal_number(m, n, k, kind, low):
+    """Products of scales around 2^low, within 2^6: a product is rounded to a multiple of 2^-149, off by at most 2^-150,
+    and so is each of the at most K / 128 + 9 additions whose result is that small (eight waves' sums among them); a bf16
+    result that small is off by half of bf16's least step 2^-133."""
+    rng = np.random.default_rng(m + n - low)
+    a, qa = operand(m, k, "line", "e5m2", rng, 2.0 ** (low // 2))
+    b, qb = operand(n, k, kind, "e4m3", rng, 2.0 ** (low - low // 2))
+    kb = a[0].shape[1] // 128
+    c, g = fp8.gemm_ref(a, "e5m2", b, "e4m3", kind)
+    codes = np.abs(fp8.decode(a[0], "e5m2")) @ np.abs(fp8.decode(b[0], "e4m3")).T
+    for bf16 in (False, True):
+        announce("fp8 small scales %dx%dx%d %s 2^%d %s" % (m, n, k, kind, low, "bf16" if bf16 else "fp32"))
+        got = fp8_gemm(qa, qb, torch.bfloat16 if bf16 else torch.float32)
+        torch.cuda.synchronize()
+        tol = tolerance(c, g, kb, bf16) + (2.0 ** -150 * codes + (kb + 9) * 2.0 ** -150) * (1 + bf16 * 2.0 ** -8)
+        tol += bf16 * 2.0 ** -134
+        assert np.all(np.abs(got.double().cpu().numpy() - c) <= tol)

@@ -68,11 +68,13 @@ def test_many_lines_take_a_tiled_kernel(plans):
 
 
 def test_shapes_of_the_gpu_tests_take_the_kernels_they_are_meant_for(plans):
-    from test_fp8_large_gpu import BIG, FAR, FAR_SHAPES, chunks
+    from test_fp8_large_gpu import BIG, FAR, FAR_SHAPES, SMALL_SCALES, chunks
     for (m, n, k), which, path in FAR_SHAPES:
         packed, far = plans([case(m, n, k), case(m, n, k, lda=FAR if which in ("a", "both") else None,
                                                  ldb=FAR if which in ("b", "both") else None, tile_scales=1 << 20)])
         assert packed[0] == far[0] == path, (m, n, k)
+    assert [g[0] for g in plans([case(*s) for s in SMALL_SCALES])] == ["few", "few", "mid", "mid", "big"]
+    assert plans([case(*SMALL_SCALES[3])])[0][1] > 1
     large = plans([case(*s) for s in BIG + [(4096, 8192, 4096)]])
     assert all(g[0] == "big" for g in large) and min(g[2] for g in large) == 1 and max(g[2] for g in large) >= 4
     for m, n, k in BIG:

@@ -148,6 +148,10 @@ __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const AdamwArgs a) {
     // the seed is fixed when a graph is captured: the device's step gives every replay draws of its own
     if (a.step.step_dev != nullptr) seed += (uint64_t)step;
   }
+  // one value for the whole wave: in scalar registers, as the ten rounds' keys made of it (in vector registers, where the
+  // loaded step would put it, 8-bit stochastic steps took 3% longer)
+  seed = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(seed >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)seed);
   const bool scaled = a.step.grad_scale != nullptr;
   const float gs = scaled ? *a.step.grad_scale : 1.0f;
   const uint32_t chunks = a.end[a.count - 1];

@@ -599,17 +599,19 @@ class AdamWTensors:
         grads = tuple(grads)
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d weights" % (len(grads), len(self.params)))
-        for i, (g, w) in enumerate(zip(grads, self.params)):
-            if not isinstance(g, torch.Tensor) or g.dtype not in (torch.float32, torch.bfloat16):
+        found = []
+        for i, (g, w) in enumerate(zip(grads, self._params)):
+            if not isinstance(g, torch.Tensor) or g.dtype not in _OUT_KINDS:
                 raise ValueError("tensor %d: its gradient must be float32 or bfloat16" % i)
-            self._hold(i, "gradient", g, g.dtype, w.numel())
+            n, kind = w.numel(), _OUT_KINDS[g.dtype]
+            self._hold(i, "gradient", g, g.dtype, n)
             start = g.data_ptr()
-            at = bisect_left(self._starts, start + g.numel() * g.element_size()) - 1
-            if at >= 0 and g.numel() and self._spans[at][1] > start:
+            at = bisect_left(self._starts, start + n * g.element_size()) - 1
+            if n and at >= 0 and self._spans[at][1] > start:
                 raise ValueError("tensors %d and %d: a gradient overlaps a weight, state or copy" % (i, self._spans[at][2]))
-        for i, g in enumerate(grads):
-            self._c[i].g = g.data_ptr()
-            self._c[i].grad = _lib.OUT["f32" if g.dtype == torch.float32 else "bf16"]
+            found.append((start, kind))
+        for c, (start, kind) in zip(self._c, found):
+            c.g, c.grad = start, kind
         self._grads = grads
 
 

@@ -20,12 +20,17 @@
 // round-to-nearest would return the old code forever.
 //
 // Memory-bound: 28 to 30 bytes per element with 32-bit moments, 16 to 18 with
-// 8-bit ones.  218 million weights (a Llama block's linears) take 1203 us with
-// 32-bit moments and fp32 gradients (5.4 TB/s) and 715 us with 8-bit ones and
-// stochastic rounding (5.5 TB/s).  A lane takes eight consecutive elements, so that 16 lanes (a
-// DPP row) hold a block of 128 and its maximum needs no LDS.  The tensors'
+// 8-bit ones.  218 million weights (a Llama block's linears) take 1208 us with
+// 32-bit moments and fp32 gradients (5.4 TB/s) and 713 to 738 us with 8-bit ones,
+// rounded either way (5.5).  A lane takes eight consecutive elements, so that 16
+// lanes (a DPP row) hold a block of 128 and its maximum needs no LDS.  The tensors'
 // addresses ride in the kernel's arguments, 48 to a launch, so a step needs no
 // table in device memory; a workgroup takes 4096 elements.
+//
+// Vector accesses need every array of a tensor at 16 bytes (8-bit moments at 8).
+// A tensor that is not so goes element by element, in 2.5 times the time: 2980 and
+// 1810 us for the weights above; 100 odd tensors of 13.6 million weights, packed
+// without padding, 194 us (32 bits) and 128 (8 bits) against 70 and 57.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

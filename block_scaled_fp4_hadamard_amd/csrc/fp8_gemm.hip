@@ -222,16 +222,19 @@ __device__ __forceinline__ const T* uniform(const T* p) {
 
 // ---------------------------------------------------------------------------
 // Few rows of A (single tokens, short batches): the operand that matters is
-// B, read once from HBM.  A workgroup takes 16 J columns of C (fp8_few_columns) and
+// B, read once.  A workgroup takes 16 J columns of C (fp8_few_columns) and
 // all M <= 16 F rows; its waves take the K blocks in turn, straight from memory
 // to registers with U blocks in flight, and their sums meet in LDS in the
 // waves' order.  Rows past M and columns past N read the last one and are not
 // stored.
 //
-// Memory-bound: one row takes 7.0 us with 6144 x 4096 (3.6 TB/s with the launch,
-// back to back in a graph), 11.1 us with 4096 x 14336 (5.3), 74 us with 28672 x
-// 14336 (5.6); sixteen rows 8.4, 15.5 and 80 us, 32 rows 10.7, 22 and 95.  Eight waves
-// rather than a split over workgroups: no second launch joins the parts.
+// Memory-bound.  Back to back in a graph, launch included, other weights each
+// time (from HBM) and the same weights again (in the 256 MB last-level cache): one
+// row takes 8.4 and 6.8 us with 6144 x 4096 (3.0 and 3.7 TB/s), 16.1 and 10.6 us
+// with 4096 x 14336 (3.7 and 5.5), 26.7 and 20.0 with 28672 x 4096 (4.4 and 5.9), 74
+// us either way with 28672 x 14336 (5.6); sixteen rows 10.0 and 8.0, 19.1 and 15.1,
+// 28.1 and 21.1, 76; 32 rows 11.8 and 10.2, 22.5 and 21.5, 32.3 and 27.2, 95.  Eight
+// waves rather than a split over workgroups: no second launch joins the parts.
 // Sixteen waves took the same or more.
 template <int AF, int BF, int KIND, int OUT, int F, int J>
 __global__ void __launch_bounds__(64 * kFewWaves) fp8_mm_few(const Fp8GemmParams p) {
@@ -639,11 +642,12 @@ __global__ void __launch_bounds__(256) fp8_mm_sum(const Fp8GemmParams p, const f
 // results are not stored), so every copy stays inside the operand and any M
 // and N run here.
 //
-// 8192 x 28672 x 4096 takes 784 us (2450 TFLOP/s), 8192 x 4096 x 14336 374 us
-// (2570) with tile scales, 921 and 434 us with line scales, whose joins need two
-// operations an element; the library's product with one scale for each whole
-// operand reaches 2680 to 3100.  The matrix cores are busy 65% of the cycles, and the
-// chip lowers its clock to 1.8 GHz for it.
+// 8192 x 28672 x 4096 takes 759 to 828 us by card (2540 to 2320 TFLOP/s), 8192 x 4096
+// x 14336 353 to 374 us (2730 to 2570) with tile scales, 899 and 425 us with line
+// scales, whose joins need two operations an element; an E5M2 gradient with an E4M3
+// weight, 8192 x 4096 x 28672, 777 us (2480).  The library's product with one scale
+// for each whole operand reaches 2680 to 3100.  The matrix cores are busy 58 to 65%
+// of the cycles, and the chip lowers its clock to 1.7 to 2.0 GHz for it.
 constexpr int kBThreads = 512;
 constexpr int kStage = kBT * kKB;
 

@@ -18,11 +18,14 @@
 // codes go through LDS (16 KB, 16-byte pieces XOR-swizzled by column) and leave
 // as whole 128-byte lines too.
 //
-// Memory-bound: 2 bytes read and 1 written per element and output.  Both axes
-// of 8192 x 4096 take 24 us (5.7 TB/s), of 28672 x 4096 (tiles) 91 us (5.2 TB/s);
-// a copy of this size class reaches 4.7 TB/s here.  The codes leave by
-// non-temporal stores, which gained 20% and 3% on these two: they stay out of
-// the way of x, which the operation before may have left in the cache; a
+// Memory-bound: 2 bytes read and 1 written per element and output.  Where every
+// call has other memory, as in a training step, both axes of 8192 x 4096 take 30
+// us (4.5 TB/s), of 28672 x 4096 (tiles) 91 us (5.2); of 8192 x 14336 the rows
+// alone 65 us (5.4), the columns alone 77 (4.6).  The same buffers cast again
+// and again, part of them in the 256 MB last-level cache: 22, 71, 52 and 53 us.
+// HBM's peak is 8 TB/s, a copy of 4 GiB reaches 4.6 to 4.7 here.  The codes leave
+// by non-temporal stores, which gained 20% and 3% on the first two: they stay out
+// of the way of x, which the operation before may have left in the cache; a
 // training step that multiplies the codes next runs the same either way.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -341,7 +341,8 @@ def _meet(x, y):
     if not (rows_p and wide_p and rows_q and wide_q):
         return False
     # each row of x against the last row of y that starts before its end: views side by side in one buffer are apart
-    start, other = p + pitch_p * torch.arange(rows_p), q + pitch_q * torch.arange(rows_q)
+    start = p + pitch_p * torch.arange(rows_p, device="cpu")
+    other = q + pitch_q * torch.arange(rows_q, device="cpu")
     last = torch.searchsorted(other, start + wide_p) - 1
     return bool(((last >= 0) & (other[last.clamp_min(0)] + wide_q > start)).any())
 

@@ -68,11 +68,11 @@ inline int fp8_splits(int64_t tiles, int64_t nk, double outputs, bool exact) {
 // pitch in floats (0 for line scales, whose pitch is added in 64 bits).  Operands beyond that run on the kernel for few
 // rows, 32 rows of A at a time.
 //
-// By measurement (bf16 output, tile scales, operands in the last-level cache): up to 32 rows of A, reading B once wins (16
-// x 6144 x 4096: 8.4 us against 16; 64 rows, as four row fragments, took 22 against 16).  Above, a K block of a full round of the chip costs about
-// 1.67 us in 256 x 256 tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU, half the work; about 0.7 us with one a
-// CU), and the fewest such times win.  fp32 output (exact) always takes the small tiles, whose wave leaves room for the
-// widened operands.
+// By measurement (bf16 output, tile scales, operands in the last-level cache): up to 32 rows of A, reading B once wins
+// (16 x 6144 x 4096: 8.4 us against 16; 64 rows, as four row fragments, took 22 against 16).  Above, a K block of a
+// full round of the chip costs about 1.67 us in 256 x 256 tiles (one a CU) and 1.15 us in 128 x 128 tiles (two a CU,
+// half the work; about 0.7 us with one a CU), and the fewest such times win.  fp32 output (exact) always takes the
+// small tiles, whose wave leaves room for the widened operands.
 inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t tile_scales, bool exact) {
   Fp8Plan plan{Fp8Path::kFew, 1, {}};
   const int64_t lim = int64_t(1) << 24;
@@ -97,9 +97,10 @@ inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ld
 // round's time goes by the operand rows that its workgroups read, B's and A's: with K 14336 (bf16 output) 10, 17, 23
 // and 29 us for 1 to 4 fragments and one row of A, 21, 29, 38 and 44 with 32 rows.  No choice reads B faster than HBM
 // gives it.  fp32 output takes longer with 3 and 4 fragments, whose widened codes leave room for half the waves.  In
-// units of 7 us there, with the weights in the last-level cache: 32 x 6144 x 14336 took 41 us in two rounds of one fragment and 29 in one of two, 16 x 28672 x
-// 14336 104, 90, 90 and 80 with 1 to 4 fragments, 98, 92, 118 and 107 to fp32.  A grid holds fewer than 2^32 threads,
-// which one fragment would pass at N = 2^27 - 1; the ABI refuses N >= 2^27.
+// units of 7 us there, the same weights again and again: 32 x 6144 x 14336 took 41 us in two rounds of one
+// fragment and 29 in one of two, 16 x 28672 x 14336 104, 90, 90 and 80 with 1 to 4 fragments, 98, 92, 118 and 107 to
+// fp32.  A grid holds fewer than 2^32 threads, which one fragment would pass at N = 2^27 - 1; the ABI refuses N >=
+// 2^27.
 inline int fp8_few_columns(int64_t M, int64_t N, bool exact) {
   const double slower[2][4] = {{1.0, 1.0, 1.3, 1.4}, {1.0, 1.0, 0.93, 1.07}};      // fp32: up to 16 rows, and above
   int best = 0;

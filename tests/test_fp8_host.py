@@ -409,3 +409,17 @@ def test_workspace_of_any_size_asked_for():
                     (300, 500, (1 << 62) - 1), (-1, 500, 4096), (300, 0, 4096), (300, 500, 0)):
         assert _lib.mx_fp8_gemm_workspace(M, N, K, 0) == _lib.mx_fp8_gemm_workspace(M, N, K, 1) == 0
     assert _lib.mx_fp8_gemm_workspace(300, 500, 8192, 2) == 0
+
+
+def test_memory_checks_stay_on_the_host():
+    """Whatever torch's default device is: a check that made its index tensors there would run on the GPU, and break a
+    capture."""
+    buf = torch.zeros(1 << 17, dtype=torch.uint8)
+    x = torch.zeros((128, 128), dtype=torch.bfloat16)
+    row, col = operand_at(buf, 0, 128, 128, pitch=256), operand_at(buf, 128, 128, 128, pitch=256)
+    over = operand_at(buf, 112, 128, 128, pitch=256)
+    with torch.device("meta"):
+        with pytest.raises(ValueError, match="CUDA"):
+            fp8_quantize(x, axis="both", row_out=row, col_out=col)
+        with pytest.raises(ValueError, match="share memory"):
+            fp8_quantize(x, axis="both", row_out=row, col_out=over)

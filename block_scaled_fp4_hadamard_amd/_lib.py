@@ -18,10 +18,12 @@ OUT = {"f32": 0, "bf16": 1}
 OSCI = {"init": 0, "track": 1, "check": 2}
 FP8_FMT = {"e4m3": 0, "e5m2": 1}
 FP8_KIND = {"line": 0, "tile": 1}
+NORM = {"layer": 0, "rms": 1}
 
 EXPORTS = ("mx_quantize", "mx_hadamard_quantize", "mx_gemm", "mx_gemm_grouped", "mx_mxnorm_quantize", "mx_quant_stats",
            "mx_nvfp4_quantize", "mx_hadamard_rotate", "mx_quantize_f32", "mx_osci_reset", "mx_fp8_quantize",
-           "mx_fp8_gemm", "mx_fp8_gemm_workspace", "mx_adamw_step", "mx_status_str", "mx_version")
+           "mx_fp8_gemm", "mx_fp8_gemm_workspace", "mx_adamw_step", "mx_layer_norm", "mx_layer_norm_grad",
+           "mx_layer_norm_grad_workspace", "mx_status_str", "mx_version")
 
 
 class MXError(RuntimeError):
@@ -108,6 +110,14 @@ def lib():
         L.mx_fp8_gemm_workspace.restype = i64
         L.mx_adamw_step.argtypes = [ctypes.POINTER(AdamwTensorC), i32, i32, ctypes.POINTER(AdamwParamsC), i32, u64, vp]
         L.mx_adamw_step.restype = ctypes.c_int
+        f64 = ctypes.c_double
+        L.mx_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f64, i32, vp, i64, vp, vp, vp]
+        L.mx_layer_norm.restype = ctypes.c_int
+        L.mx_layer_norm_grad.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, vp, vp, i32, vp, i64, vp, vp, vp, i64,
+                                         vp]
+        L.mx_layer_norm_grad.restype = ctypes.c_int
+        L.mx_layer_norm_grad_workspace.argtypes = [i64, i64, i32, i32]
+        L.mx_layer_norm_grad_workspace.restype = i64
         L.mx_status_str.argtypes = [ctypes.c_int]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_version.argtypes = []

@@ -652,3 +652,126 @@ def adamw_step(tensors, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
     else:
         _launch(dev.index if dev.type == "cuda" else -1, "mx_adamw_step", _lib.lib().mx_adamw_step, *args)
         _written(tensors._written)
+
+
+_NORM = _lib.NORM
+
+
+def _matrix(x, name, at=None):
+    """(rows, cols, pitch, type) of a 2-D row-major float32 or bfloat16 CUDA tensor, on CUDA device number `at`."""
+    if x.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    kind = _OUT_KINDS.get(x.dtype)
+    if kind is None:
+        raise ValueError("%s must be float32 or bfloat16, got %s" % (name, x.dtype))
+    if at is not None and x.get_device() != at:
+        raise ValueError("%s is on another device" % name)
+    rows, cols = x.shape
+    return rows, cols, _pitch(x.stride(), rows, cols, name), kind
+
+
+def _vector(x, n, dtypes, name, at):
+    """The address of a contiguous tensor of n elements on CUDA device number `at`."""
+    if x.dtype not in dtypes or x.numel() != n or not x.is_contiguous() or x.get_device() != at:
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on the input's device"
+                         % (name, " or ".join(str(d) for d in dtypes), n))
+    return x.data_ptr()
+
+
+def _apart(out, others):
+    """ValueError where the 2-D tensor `out` shares memory with one of others: (name, tensor or None), each 2-D or
+    contiguous."""
+    def region(x):
+        size = x.element_size()
+        if x.dim() == 2:
+            return x.data_ptr(), x.shape[0], size * x.shape[1], size * x.stride(0)
+        return x.data_ptr(), 1, size * x.numel(), size * x.numel()
+    mine = region(out)
+    for name, x in others:
+        if x is not None and _meet(mine, region(x)):
+            raise ValueError("out and %s share memory" % name)
+
+
+_F32, _FLOATS = (torch.float32,), (torch.float32, torch.bfloat16)
+
+
+def _norm_weights(weight, bias, cols, at):
+    """(address of weight, of bias, their type)."""
+    if weight is None and bias is None:
+        return None, None, 0
+    given = weight if weight is not None else bias
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one type")
+    return (_vector(weight, cols, _FLOATS, "weight", at) if weight is not None else None,
+            _vector(bias, cols, _FLOATS, "bias", at) if bias is not None else None, _OUT_KINDS[given.dtype])
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, kind="layer", out=None):
+    """Layer norm of the rows of a 2-D float32 or bfloat16 CUDA tensor, or (kind "rms") its RMS form, which takes no mean
+    and no bias: (y, mean, rstd), y in x's type, the rows' float32 statistics for layer_norm_grad (mean None for "rms").
+
+    weight and bias: cols elements of one type, float32 or bfloat16 (None: ones, zeros).  out: y's place, apart from the
+    inputs.
+    """
+    if kind not in _NORM:
+        raise ValueError("unknown kind %r" % (kind,))
+    rows, cols, ld, dtype = _matrix(x, "x")
+    at = x.get_device()
+    if kind == "rms" and bias is not None:
+        raise ValueError("kind 'rms' takes no bias")
+    w, b, wtype = _norm_weights(weight, bias, cols, at)
+    if out is None:
+        y, ld_y = x.new_empty((rows, cols)), cols
+    else:
+        y = out
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must be a %s view of shape (%d, %d)" % (x.dtype, rows, cols))
+        ld_y = _matrix(out, "out", at)[2]
+        _apart(out, (("x", x), ("weight", weight), ("bias", bias)))
+    mean = x.new_empty(rows, dtype=torch.float32) if kind == "layer" else None
+    rstd = x.new_empty(rows, dtype=torch.float32)
+    _launch(at, "mx_layer_norm", _lib.lib().mx_layer_norm, x.data_ptr(), dtype, rows, cols, ld, w, b, wtype, eps,
+            _NORM[kind], y.data_ptr(), ld_y, mean.data_ptr() if mean is not None else None, rstd.data_ptr())
+    if out is not None:
+        _written(out)
+    return y, mean, rstd
+
+
+def layer_norm_grad(dy, x, mean, rstd, weight=None, kind="layer", out=None, sums=True):
+    """The backward pass of layer_norm for y's gradient dy: (dx, dweight, dbias), dx in x's type, the other two float32
+    sums over the rows (dbias None for kind "rms"; both None where sums is false).
+
+    x, weight and kind are the forward pass's, mean and rstd its results.  out: dx's place, apart from the inputs.
+    """
+    if kind not in _NORM:
+        raise ValueError("unknown kind %r" % (kind,))
+    rows, cols, ld, dtype = _matrix(x, "x")
+    at = x.get_device()
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must be a %s tensor of shape (%d, %d)" % (x.dtype, rows, cols))
+    ld_dy = _matrix(dy, "dy", at)[2]
+    if (mean is None) != (kind == "rms"):
+        raise ValueError("mean comes with kind 'layer' and with no other")
+    w, _, wtype = _norm_weights(weight, None, cols, at)
+    m = _vector(mean, rows, _F32, "mean", at) if mean is not None else None
+    r = _vector(rstd, rows, _F32, "rstd", at)
+    if out is None:
+        dx, ld_dx = x.new_empty((rows, cols)), cols
+    else:
+        dx = out
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must be a %s view of shape (%d, %d)" % (x.dtype, rows, cols))
+        ld_dx = _matrix(out, "out", at)[2]
+        _apart(out, (("dy", dy), ("x", x), ("weight", weight), ("mean", mean), ("rstd", rstd)))
+    dweight = x.new_empty(cols, dtype=torch.float32) if sums else None
+    dbias = x.new_empty(cols, dtype=torch.float32) if sums and kind == "layer" else None
+    lib = _lib.lib()
+    # the workspace is this call's own: held until the launch, its memory then goes to later work of this stream only
+    size = lib.mx_layer_norm_grad_workspace(rows, cols, dtype, sums)
+    space = x.new_empty(size, dtype=torch.uint8) if size else None
+    _launch(at, "mx_layer_norm_grad", lib.mx_layer_norm_grad, dy.data_ptr(), ld_dy, x.data_ptr(), ld, dtype, rows, cols, w,
+            wtype, m, r, _NORM[kind], dx.data_ptr(), ld_dx, dweight.data_ptr() if dweight is not None else None,
+            dbias.data_ptr() if dbias is not None else None, space.data_ptr() if size else None, size)
+    if out is not None:
+        _written(out)
+    return dx, dweight, dbias

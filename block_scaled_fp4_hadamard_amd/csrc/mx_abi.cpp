@@ -7,6 +7,7 @@
 #include <math.h>
 #include "mx_kernels.h"
 #include "fp8_kernels.h"
+#include "norm_kernels.h"
 
 namespace {
 
@@ -39,6 +40,15 @@ mx_status check_qtensor(const mx_qtensor* q, int64_t lines, int64_t k, int32_t b
   if (q->ld_codes < k / 2 || q->ld_scales < k / block) return MX_ERR_INVALID;
   if (lines > 1 && (q->ld_codes <= 0 || q->ld_scales <= 0)) return MX_ERR_INVALID;
   return MX_OK;
+}
+
+bool out_ok(int type) { return type == MX_OUT_F32 || type == MX_OUT_BF16; }
+bool norm_kind_ok(int kind) { return kind == MX_NORM_LAYER || kind == MX_NORM_RMS; }
+bool norm_sizes_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows < (int64_t(1) << 40) && cols < (int64_t(1) << 30);
+}
+bool norm_rows_ok(const void* x, int type, int64_t ld, int64_t cols) {
+  return x != nullptr && ((uintptr_t)x & (type == MX_OUT_F32 ? 3u : 1u)) == 0 && ld >= cols;
 }
 
 mx_status quantize_impl(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, int32_t block, int grid,
@@ -550,6 +560,51 @@ mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t b
     if (e != hipSuccess) return MX_ERR_DEVICE;
   }
   return MX_OK;
+}
+
+mx_status mx_layer_norm(const void* x, mx_out type, int64_t rows, int64_t cols, int64_t ld_x, const void* weight,
+                        const void* bias, mx_out weight_type, double eps, mx_norm_kind kind, void* y, int64_t ld_y,
+                        float* mean, float* rstd, void* hip_stream) {
+  if (!out_ok(type) || !out_ok(weight_type) || !norm_kind_ok(kind) || !norm_sizes_ok(rows, cols)) return MX_ERR_INVALID;
+  if (!(eps >= 0.0) || !isfinite((float)eps)) return MX_ERR_INVALID;
+  if (kind == MX_NORM_RMS && (bias != nullptr || mean != nullptr)) return MX_ERR_INVALID;
+  if (rows == 0 || cols == 0) return MX_OK;
+  if (!norm_rows_ok(x, type, ld_x, cols) || !norm_rows_ok(y, type, ld_y, cols)) return MX_ERR_INVALID;
+  const uintptr_t wmask = weight_type == MX_OUT_F32 ? 3u : 1u;
+  if (((uintptr_t)weight & wmask) || ((uintptr_t)bias & wmask)) return MX_ERR_INVALID;
+  if (((uintptr_t)mean & 3u) || ((uintptr_t)rstd & 3u)) return MX_ERR_INVALID;
+  const mx::NormParams p{x, weight, bias, rows, cols, ld_x, (float)eps, y, ld_y, mean, rstd};
+  const hipError_t e = mx::launch_norm(p, type, weight_type, kind, (hipStream_t)hip_stream);
+  return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+int64_t mx_layer_norm_grad_workspace(int64_t rows, int64_t cols, mx_out type, int32_t sums) {
+  if (!out_ok(type) || !norm_sizes_ok(rows, cols) || rows == 0 || cols == 0) return 0;
+  return mx::norm_grad_workspace(rows, cols, type, sums != 0);
+}
+
+mx_status mx_layer_norm_grad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, mx_out type, int64_t rows,
+                             int64_t cols, const void* weight, mx_out weight_type, const float* mean,
+                             const float* rstd, mx_norm_kind kind, void* dx, int64_t ld_dx, float* dweight,
+                             float* dbias, void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (!out_ok(type) || !out_ok(weight_type) || !norm_kind_ok(kind) || !norm_sizes_ok(rows, cols)) return MX_ERR_INVALID;
+  if (kind == MX_NORM_RMS && mean != nullptr) return MX_ERR_INVALID;
+  if (((uintptr_t)dweight & 3u) || ((uintptr_t)dbias & 3u)) return MX_ERR_INVALID;
+  if (cols == 0) return MX_OK;
+  if (rows > 0) {
+    if (!norm_rows_ok(dy, type, ld_dy, cols) || !norm_rows_ok(x, type, ld_x, cols) ||
+        !norm_rows_ok(dx, type, ld_dx, cols))
+      return MX_ERR_INVALID;
+    if ((uintptr_t)weight & (weight_type == MX_OUT_F32 ? 3u : 1u)) return MX_ERR_INVALID;
+    if (rstd == nullptr || ((uintptr_t)rstd & 3u) || ((uintptr_t)mean & 3u)) return MX_ERR_INVALID;
+    if (kind == MX_NORM_LAYER && mean == nullptr) return MX_ERR_INVALID;
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    const int64_t need = mx::norm_grad_workspace(rows, cols, type, sums);
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)) return MX_ERR_INVALID;
+  }
+  const mx::NormGradParams p{dy, x, weight, mean, rstd, rows, cols, ld_dy, ld_x, ld_dx, dx, dweight, dbias};
+  const hipError_t e = mx::launch_norm_grad(p, type, weight_type, kind, (float*)workspace, (hipStream_t)hip_stream);
+  return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
 }
 
 const char* mx_status_str(mx_status status) {

@@ -498,6 +498,62 @@ typedef struct {
 mx_status mx_adamw_step(const mx_adamw_tensor *tensors, int32_t count, int32_t bits,
                         const mx_adamw_params *params, mx_round round, uint64_t seed, void *hip_stream);
 
+/*
+ * Layer norm of the rows of a matrix and its RMS form: the norms in front of a
+ * block's linears, exactly; mx_mxnorm_quantize estimates the second one from
+ * block maxima ("MXNorm: Reusing MXFP block scales ...", Metodologia 2).
+ *   MX_NORM_LAYER  mean = sum x / cols, d = x - mean, y = d * rstd * weight + bias
+ *   MX_NORM_RMS    mean = 0, d = x, y = d * rstd * weight
+ *   rstd = 1 / sqrt(sum d^2 / cols + eps)
+ * in float32, y rounded to its type once (bf16: to nearest even).
+ */
+typedef enum { MX_NORM_LAYER = 0, MX_NORM_RMS = 1 } mx_norm_kind;
+
+/*
+ * mx_layer_norm: y and the rows' statistics.
+ *   x, y       device, row-major, both of `type`, aligned to it; rows ld_x and
+ *              ld_y elements apart, >= cols (16-byte aligned rows: fastest);
+ *              y must not overlap x
+ *   rows, cols either 0: nothing to do, MX_OK; rows < 2^40, cols < 2^30
+ *   weight, bias  device, cols elements of `weight_type`; NULL: ones, zeros;
+ *              bias is NULL for MX_NORM_RMS
+ *   eps        finite, >= 0 (with 0 a constant row, or an RMS row of zeros,
+ *              becomes NaN)
+ *   mean, rstd device float32 [rows], what mx_layer_norm_grad takes, or NULL;
+ *              mean is NULL for MX_NORM_RMS
+ * A row that holds NaN becomes NaN; one that holds Inf becomes NaN (MX_NORM_LAYER), or has rstd 0, zeros where x is
+ * finite and NaN where it is not (MX_NORM_RMS).
+ */
+mx_status mx_layer_norm(const void *x, mx_out type, int64_t rows, int64_t cols, int64_t ld_x, const void *weight,
+                        const void *bias, mx_out weight_type, double eps, mx_norm_kind kind, void *y, int64_t ld_y,
+                        float *mean, float *rstd, void *hip_stream);
+
+/*
+ * mx_layer_norm_grad: the backward pass of mx_layer_norm for the gradient dy of
+ * y.  With h = (x - mean) * rstd and g = dy * weight,
+ *   dx      = rstd * (g - sum(g) / cols - h * sum(g * h) / cols)   (MX_NORM_RMS:
+ *             without sum(g) / cols)
+ *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy
+ * in float32, dx rounded to its type once.
+ *   dy, x, dx  as x and y above, of one type; dx must overlap no input
+ *   mean, rstd the forward pass's (mean NULL for MX_NORM_RMS)
+ *   weight     as above
+ *   dweight, dbias  device float32 [cols], written (zeros with no rows), or
+ *              NULL where not wanted; both may be wanted for either kind
+ *   workspace  16-byte aligned device memory of at least
+ *              mx_layer_norm_grad_workspace bytes, this call's alone until it
+ *              has run; it needs no initial value
+ * Sums over rows have a fixed order: results depend on the arguments alone.
+ */
+mx_status mx_layer_norm_grad(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x, mx_out type, int64_t rows,
+                             int64_t cols, const void *weight, mx_out weight_type, const float *mean,
+                             const float *rstd, mx_norm_kind kind, void *dx, int64_t ld_dx, float *dweight,
+                             float *dbias, void *workspace, int64_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace that mx_layer_norm_grad needs; sums: whether dweight or dbias is wanted (0 also for sizes or a
+ * type that it refuses). */
+int64_t mx_layer_norm_grad_workspace(int64_t rows, int64_t cols, mx_out type, int32_t sums);
+
 /* A static, human-readable name for a status code. */
 const char *mx_status_str(mx_status status);
 

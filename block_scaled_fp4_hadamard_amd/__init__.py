@@ -10,3 +10,4 @@ from .api import QTensor, quantize, gemm, gemm_grouped, empty_qtensor, mxnorm_qu
 from .api import Fp8Tensor, fp8_quantize, fp8_gemm, empty_fp8  # noqa: F401
 from .api import AdamWState, AdamWTensors, adamw_step  # noqa: F401
 from .api import layer_norm, layer_norm_grad  # noqa: F401
+from .api import MuonTensors, muon_step, orthogonalize  # noqa: F401

@@ -19,11 +19,13 @@ OSCI = {"init": 0, "track": 1, "check": 2}
 FP8_FMT = {"e4m3": 0, "e5m2": 1}
 FP8_KIND = {"line": 0, "tile": 1}
 NORM = {"layer": 0, "rms": 1}
+ADJUST = {"plain": 0, "rms": 1, "shape": 2}
 
 EXPORTS = ("mx_quantize", "mx_hadamard_quantize", "mx_gemm", "mx_gemm_grouped", "mx_mxnorm_quantize", "mx_quant_stats",
            "mx_nvfp4_quantize", "mx_hadamard_rotate", "mx_quantize_f32", "mx_osci_reset", "mx_fp8_quantize",
            "mx_fp8_gemm", "mx_fp8_gemm_workspace", "mx_adamw_step", "mx_layer_norm", "mx_layer_norm_grad",
-           "mx_layer_norm_grad_workspace", "mx_status_str", "mx_version")
+           "mx_layer_norm_grad_workspace", "mx_orthogonalize", "mx_orthogonalize_workspace", "mx_muon_step",
+           "mx_muon_workspace", "mx_status_str", "mx_version")
 
 
 class MXError(RuntimeError):
@@ -58,6 +60,27 @@ class AdamwParamsC(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
                 ("step_dev", ctypes.c_void_p), ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
+class OrthoParamsC(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double), ("eps", ctypes.c_double),
+                ("steps", ctypes.c_int32)]
+
+
+class OrthoMatrixC(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld_g", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("grad", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class MuonTensorC(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("grad", ctypes.c_int32)]
+
+
+class MuonParamsC(ctypes.Structure):
+    _fields_ = [("ortho", OrthoParamsC), ("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
 GEMM_GROUP_MAX = 8      # MX_GEMM_GROUP_MAX
@@ -118,6 +141,16 @@ def lib():
         L.mx_layer_norm_grad.restype = ctypes.c_int
         L.mx_layer_norm_grad_workspace.argtypes = [i64, i64, i32, i32]
         L.mx_layer_norm_grad_workspace.restype = i64
+        mp, op = ctypes.POINTER(OrthoMatrixC), ctypes.POINTER(OrthoParamsC)
+        L.mx_orthogonalize.argtypes = [mp, i32, op, vp, i64, vp]
+        L.mx_orthogonalize.restype = ctypes.c_int
+        L.mx_orthogonalize_workspace.argtypes = [mp, i32]
+        L.mx_orthogonalize_workspace.restype = i64
+        tp = ctypes.POINTER(MuonTensorC)
+        L.mx_muon_step.argtypes = [tp, i32, ctypes.POINTER(MuonParamsC), vp, i64, vp]
+        L.mx_muon_step.restype = ctypes.c_int
+        L.mx_muon_workspace.argtypes = [tp, i32]
+        L.mx_muon_workspace.restype = i64
         L.mx_status_str.argtypes = [ctypes.c_int]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_version.argtypes = []

@@ -667,7 +667,8 @@ def _matrix(x, name, at=None):
     if at is not None and x.get_device() != at:
         raise ValueError("%s is on another device" % name)
     rows, cols = x.shape
-    return rows, cols, _pitch(x.stride(), rows, cols, name), kind
+    # an empty matrix may have any strides
+    return rows, cols, _pitch(x.stride(), rows, cols, name) if rows and cols else cols, kind
 
 
 def _vector(x, n, dtypes, name, at):
@@ -775,3 +776,157 @@ def layer_norm_grad(dy, x, mean, rstd, weight=None, kind="layer", out=None, sums
     if out is not None:
         _written(out)
     return dx, dweight, dbias
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)      # a, b, c: five steps take nearly every singular value into 0.68 .. 1.13
+
+
+def _ortho_params(steps, coefficients, eps):
+    a, b, c = coefficients
+    return _lib.OrthoParamsC(a, b, c, eps, steps)
+
+
+def orthogonalize(g, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out_dtype=torch.bfloat16, out=None):
+    """Newton-Schulz orthogonalization of a 2-D float32 or bfloat16 CUDA tensor, or of each of a list: the matrix with the
+    singular vectors of g and singular values near 1, from `steps` steps X <- a X + (b A + c A A) X, A = X X^T,
+    coefficients (a, b, c), on X = g / (|g| + eps).
+
+    A list's matrices, all on one device, are worked on together, which fills the chip where each alone does not.  The
+    products take float16 operands; the result is off by up to about 2e-3 of its norm before it is rounded to out_dtype
+    (float32 or bfloat16).  out: the result's place (a list for a list), apart from every g and from one another.
+    """
+    single = isinstance(g, torch.Tensor)
+    gs = [g] if single else list(g)
+    if not gs:
+        return []
+    at = gs[0].get_device()
+    if out is None:
+        outs = [x.new_empty(x.shape, dtype=out_dtype) for x in gs]
+    else:
+        outs = [out] if single else list(out)
+        if len(outs) != len(gs):
+            raise ValueError("%d outputs for %d matrices" % (len(outs), len(gs)))
+    array = (_lib.OrthoMatrixC * len(gs))()
+    for i, (x, o, c) in enumerate(zip(gs, outs, array)):
+        name = "matrix %d" % i
+        c.rows, c.cols, c.ld_g, c.grad = _matrix(x, name, at)
+        c.g = x.data_ptr()
+        if o.shape != x.shape:
+            raise ValueError("the output of %s must have shape %s" % (name, tuple(x.shape)))
+        _, _, c.ld_out, c.type = _matrix(o, "the output of " + name, at)
+        c.out = o.data_ptr()
+    if out is not None:
+        for i, o in enumerate(outs):
+            _apart(o, [("matrix %d" % j, x) for j, x in enumerate(gs)] + [("out %d" % j, x) for j, x in enumerate(outs[:i])])
+    lib = _lib.lib()
+    # the workspace is this call's own: held until the launches, its memory then goes to later work of this stream only
+    size = lib.mx_orthogonalize_workspace(array, len(gs))
+    space = gs[0].new_empty(size, dtype=torch.uint8) if size else None
+    _launch(at, "mx_orthogonalize", lib.mx_orthogonalize, array, len(gs), _ortho_params(steps, coefficients, eps),
+            space.data_ptr() if size else None, size)
+    if out is not None:
+        _written(outs)
+    return outs[0] if single else outs
+
+
+class MuonTensors:
+    """The matrices that muon_step updates, checked and laid out once: float32 weights, their gradients (float32 or bf16),
+    their float32 momenta and, if given, the bf16 copies that a step writes.  All are 2-D and contiguous.
+
+    None that a step writes may share memory with another or with a gradient.  The object holds the tensors it was given:
+    params, grads, momenta and copies are read-only, and a tensor whose storage is replaced (Tensor.data, resize_) needs a
+    new object.  New gradient tensors go in by set_grads.
+    """
+    params = property(lambda self: self._params)
+    grads = property(lambda self: self._grads)
+    momenta = property(lambda self: self._momenta)
+    copies = property(lambda self: self._copies)
+    device = property(lambda self: self._device)
+
+    def __init__(self, params, grads, momenta, copies=None):
+        self._params, self._momenta = tuple(params), tuple(momenta)
+        self._copies = tuple(copies) if copies is not None else (None,) * len(self._params)
+        if not len(self._params) == len(self._momenta) == len(self._copies):
+            raise ValueError("params, momenta and copies must have the same length")
+        self._device = self._params[0].device if self._params else None
+        self._c = (_lib.MuonTensorC * max(1, len(self._params)))()
+        self._written = []        # every tensor a step writes
+        spans = []                # (first byte, byte past the last, tensor) of each
+        for i, (w, m, h, c) in enumerate(zip(self._params, self._momenta, self._copies, self._c)):
+            if not isinstance(w, torch.Tensor) or w.dim() != 2:
+                raise ValueError("tensor %d: its weight must be a matrix" % i)
+            for name, x, dtype in (("weight", w, torch.float32), ("momentum", m, torch.float32),
+                                   ("copy", h, torch.bfloat16)):
+                if name == "copy" and x is None:
+                    continue
+                self._hold(i, name, x, dtype, w.shape)
+                self._written.append(x)
+                if x.numel():
+                    spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i))
+            c.w, c.m, c.copy = w.data_ptr(), m.data_ptr(), h.data_ptr() if h is not None else None
+            c.rows, c.cols = w.shape
+        spans.sort()
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("tensors %d and %d: a weight, momentum or copy overlaps another" % (i, j))
+        self._starts, self._spans = [start for start, _, _ in spans], spans
+        self.set_grads(grads)
+
+    def _hold(self, i, name, x, dtype, shape):
+        if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or not x.is_contiguous():
+            raise ValueError("tensor %d: its %s must be a contiguous %s tensor of shape %s" % (i, name, dtype, tuple(shape)))
+        if x.device != self._device:
+            raise ValueError("tensor %d: its %s is on %s, the first weight on %s" % (i, name, x.device, self._device))
+
+    def set_grads(self, grads):
+        """Other gradient tensors for the steps to come."""
+        grads = tuple(grads)
+        if len(grads) != len(self._params):
+            raise ValueError("%d gradients for %d weights" % (len(grads), len(self._params)))
+        found = []
+        for i, (g, w) in enumerate(zip(grads, self._params)):
+            if not isinstance(g, torch.Tensor) or g.dtype not in _OUT_KINDS:
+                raise ValueError("tensor %d: its gradient must be float32 or bfloat16" % i)
+            self._hold(i, "gradient", g, g.dtype, w.shape)
+            start, size = g.data_ptr(), g.numel() * g.element_size()
+            at = bisect_left(self._starts, start + size) - 1
+            if size and at >= 0 and self._spans[at][1] > start:
+                raise ValueError("tensors %d and %d: a gradient overlaps a weight, momentum or copy"
+                                 % (i, self._spans[at][2]))
+            found.append((start, _OUT_KINDS[g.dtype]))
+        for c, (start, kind) in zip(self._c, found):
+            c.g, c.grad = start, kind
+        self._grads = grads
+
+
+def muon_step(tensors, lr, momentum=0.95, weight_decay=0.1, nesterov=True, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7,
+              adjust="rms", grad_scale=None):
+    """One Muon step in place on a MuonTensors: momenta, weights and copies.  The momentum (with Nesterov's look ahead)
+    is orthogonalized as orthogonalize does it, and the weights move by lr times that, after decoupled weight decay.
+
+    adjust scales the update: "rms" by 0.2 sqrt(max(rows, cols)), to the size of an AdamW update, "shape" by
+    sqrt(max(1, rows / cols)), "plain" not at all.  lr is a number, or a one-element float32 CUDA tensor that the kernel
+    reads, so that a captured graph replays with a rate that moves on.  grad_scale: a one-element float32 CUDA tensor that
+    every gradient is multiplied by first (clipping, loss scaling).  Vectors and tables take adamw_step.
+    """
+    if adjust not in _lib.ADJUST:
+        raise ValueError("unknown adjust %r" % (adjust,))
+    dev = tensors.device
+    lr, lr_dev = _scalar(lr, torch.float32, "lr", dev)
+    scale = None
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor):
+            raise ValueError("grad_scale must be a one-element torch.float32 tensor on %s" % dev)
+        _, scale = _scalar(grad_scale, torch.float32, "grad_scale", dev)
+    params = _lib.MuonParamsC(_ortho_params(steps, coefficients, eps), lr, momentum, weight_decay, bool(nesterov),
+                              _lib.ADJUST[adjust], lr_dev, scale)
+    lib, count = _lib.lib(), len(tensors.params)
+    if dev is None:
+        _lib.check(lib.mx_muon_step(tensors._c, 0, params, None, 0, None), "mx_muon_step")   # an empty list: only the checks
+        return
+    # the workspace is this call's own: held until the launches, its memory then goes to later work of this stream only
+    size = lib.mx_muon_workspace(tensors._c, count)
+    space = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _launch(dev.index if dev.type == "cuda" else -1, "mx_muon_step", lib.mx_muon_step, tensors._c, count, params,
+            space.data_ptr() if size else None, size)
+    _written(tensors._written)

@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["quant.hip", "gemm.hip", "mxnorm.hip", "diag.hip", "nvfp4.hip", "osci.hip", "fp8_quant.hip", "fp8_gemm.hip",
-           "adamw.hip", "norm.hip", "mx_abi.cpp"]
+           "adamw.hip", "norm.hip", "ortho.hip", "mx_abi.cpp"]
 PROBE_SOURCES = ["probe/mfma_rate.hip", "probe/valu_rate.hip"]
 PROBE_LIB = os.path.join(PKG, "libmxprobe.so")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",

@@ -8,6 +8,7 @@
 #include "mx_kernels.h"
 #include "fp8_kernels.h"
 #include "norm_kernels.h"
+#include "ortho_kernels.h"
 
 namespace {
 
@@ -49,6 +50,29 @@ bool norm_sizes_ok(int64_t rows, int64_t cols) {
 }
 bool norm_rows_ok(const void* x, int type, int64_t ld, int64_t cols) {
   return x != nullptr && ((uintptr_t)x & (type == MX_OUT_F32 ? 3u : 1u)) == 0 && ld >= cols;
+}
+
+bool ortho_sizes_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows < mx::kOrthoSide && cols < mx::kOrthoSide &&
+         (rows < cols ? rows : cols) < mx::kOrthoMinor;
+}
+
+// The most that a group of the list needs, over entries of `rows(i)` x `cols(i)`; empty ones take no part.
+template <typename T>
+int64_t ortho_workspace(const T* list, int32_t count) {
+  if (count < 0 || (count > 0 && list == nullptr)) return 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (!ortho_sizes_ok(list[i].rows, list[i].cols)) return 0;
+  int64_t most = 0;
+  mx::each_ortho_group(list, count, [&](const int32_t*, int, int64_t bytes) {
+    most = bytes > most ? bytes : most;
+    return true;
+  });
+  return most;
+}
+
+bool ortho_params_ok(const mx_ortho_params& p) {
+  return p.steps >= 1 && p.steps <= 64 && p.eps > 0.0 && isfinite(p.eps) && mx::ortho_fits(p.a, p.b, p.c, p.steps);
 }
 
 mx_status quantize_impl(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, int32_t block, int grid,
@@ -604,6 +628,101 @@ mx_status mx_layer_norm_grad(const void* dy, int64_t ld_dy, const void* x, int64
   }
   const mx::NormGradParams p{dy, x, weight, mean, rstd, rows, cols, ld_dy, ld_x, ld_dx, dx, dweight, dbias};
   const hipError_t e = mx::launch_norm_grad(p, type, weight_type, kind, (float*)workspace, (hipStream_t)hip_stream);
+  return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+int64_t mx_orthogonalize_workspace(const mx_ortho_matrix* matrices, int32_t count) {
+  return ortho_workspace(matrices, count);
+}
+
+int64_t mx_muon_workspace(const mx_muon_tensor* tensors, int32_t count) { return ortho_workspace(tensors, count); }
+
+mx_status mx_orthogonalize(const mx_ortho_matrix* matrices, int32_t count, const mx_ortho_params* params,
+                           void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (count < 0 || (count > 0 && matrices == nullptr) || params == nullptr) return MX_ERR_INVALID;
+  if (!ortho_params_ok(*params)) return MX_ERR_INVALID;
+  for (int32_t i = 0; i < count; ++i) {
+    const mx_ortho_matrix& t = matrices[i];
+    if (!ortho_sizes_ok(t.rows, t.cols) || !out_ok(t.grad) || !out_ok(t.type)) return MX_ERR_INVALID;
+    if (t.rows == 0 || t.cols == 0) continue;
+    if (!norm_rows_ok(t.g, t.grad, t.ld_g, t.cols) || !norm_rows_ok(t.out, t.type, t.ld_out, t.cols))
+      return MX_ERR_INVALID;
+  }
+  const int64_t need = ortho_workspace(matrices, count);
+  if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)) return MX_ERR_INVALID;
+  mx::OrthoStep step{};
+  step.a = params->a;
+  step.b = params->b;
+  step.c = params->c;
+  step.eps = params->eps;
+  step.steps = params->steps;
+  hipError_t e = hipSuccess;
+  mx::each_ortho_group(matrices, count, [&](const int32_t* at, int n, int64_t) {
+    mx::OrthoItem items[mx::kOrthoGroup];
+    uint8_t* space = (uint8_t*)workspace;
+    for (int i = 0; i < n; ++i) {
+      const mx_ortho_matrix& t = matrices[at[i]];
+      items[i] = mx::OrthoItem{t.g, nullptr, nullptr, nullptr, t.out, space, t.ld_g, t.ld_out, (int)t.rows, (int)t.cols,
+                               t.grad == MX_OUT_BF16, t.type == MX_OUT_BF16, 1.0f};
+      space += mx::ortho_size(t.rows, t.cols).bytes;
+    }
+    e = mx::launch_ortho(items, n, step, (hipStream_t)hip_stream);
+    return e == hipSuccess;
+  });
+  return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
+}
+
+mx_status mx_muon_step(const mx_muon_tensor* tensors, int32_t count, const mx_muon_params* params, void* workspace,
+                       int64_t workspace_bytes, void* hip_stream) {
+  if (count < 0 || (count > 0 && tensors == nullptr) || params == nullptr) return MX_ERR_INVALID;
+  const mx_muon_params& q = *params;
+  if (!ortho_params_ok(q.ortho) || !(q.momentum >= 0.0 && q.momentum < 1.0)) return MX_ERR_INVALID;
+  // as the float32 that the kernels take
+  if (!((float)q.momentum < 1.0f) || !isfinite(q.weight_decay) || (q.nesterov != 0 && q.nesterov != 1))
+    return MX_ERR_INVALID;
+  if (q.adjust != MX_MUON_PLAIN && q.adjust != MX_MUON_RMS && q.adjust != MX_MUON_SHAPE) return MX_ERR_INVALID;
+  if (q.lr_dev == nullptr ? !isfinite(q.lr) : ((uintptr_t)q.lr_dev & 3u) != 0) return MX_ERR_INVALID;
+  if (((uintptr_t)q.grad_scale & 3u) != 0) return MX_ERR_INVALID;
+  for (int32_t i = 0; i < count; ++i) {
+    const mx_muon_tensor& t = tensors[i];
+    if (!ortho_sizes_ok(t.rows, t.cols) || !out_ok(t.grad)) return MX_ERR_INVALID;
+    if (t.rows == 0 || t.cols == 0) continue;
+    if (!norm_rows_ok(t.g, t.grad, t.cols, t.cols) || !norm_rows_ok(t.w, MX_OUT_F32, t.cols, t.cols) ||
+        !norm_rows_ok(t.m, MX_OUT_F32, t.cols, t.cols) || ((uintptr_t)t.copy & 1u))
+      return MX_ERR_INVALID;
+  }
+  const int64_t need = ortho_workspace(tensors, count);
+  if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)) return MX_ERR_INVALID;
+  mx::OrthoStep step{};
+  step.a = q.ortho.a;
+  step.b = q.ortho.b;
+  step.c = q.ortho.c;
+  step.eps = q.ortho.eps;
+  step.steps = q.ortho.steps;
+  step.momentum = (float)q.momentum;
+  step.rest = (float)(1.0 - q.momentum);
+  step.nesterov = q.nesterov != 0;
+  step.lr = q.lr;
+  step.weight_decay = q.weight_decay;
+  step.lr_dev = q.lr_dev;
+  step.grad_scale = q.grad_scale;
+  hipError_t e = hipSuccess;
+  mx::each_ortho_group(tensors, count, [&](const int32_t* at, int n, int64_t) {
+    mx::OrthoItem items[mx::kOrthoGroup];
+    uint8_t* space = (uint8_t*)workspace;
+    for (int i = 0; i < n; ++i) {
+      const mx_muon_tensor& t = tensors[at[i]];
+      const double r = (double)t.rows, c = (double)t.cols;
+      const double scale = q.adjust == MX_MUON_RMS     ? 0.2 * sqrt(r > c ? r : c)
+                           : q.adjust == MX_MUON_SHAPE ? sqrt(r > c ? r / c : 1.0)
+                                                       : 1.0;
+      items[i] = mx::OrthoItem{t.g, t.m, t.w, t.copy, nullptr, space, t.cols, 0, (int)t.rows, (int)t.cols,
+                               t.grad == MX_OUT_BF16, false, scale};
+      space += mx::ortho_size(t.rows, t.cols).bytes;
+    }
+    e = mx::launch_ortho(items, n, step, (hipStream_t)hip_stream);
+    return e == hipSuccess;
+  });
   return e == hipSuccess ? MX_OK : MX_ERR_DEVICE;
 }
 

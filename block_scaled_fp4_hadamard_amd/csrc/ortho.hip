@@ -1,0 +1,573 @@
+// Orthogonalizing matrices by Newton-Schulz steps, alone or as the update of a
+// Muon step.  From X = U / (|U| + eps), |.| the Frobenius norm, each step takes
+//
+//   A = X X^T,   B = b A + c A A,   X <- a X + B X
+//
+// which sends every singular value s of X to a s + b s^3 + c s^5: small ones
+// grow by a factor a, and all end near 1.  X is held with its shorter side as
+// rows (U or its transpose), so that A and B are small.  In the last step B
+// takes a on its diagonal and X <- B X is all.
+//
+// Number formats.  The products are float16 with float32 sums: 11 bits at the
+// rate of bf16's 8, and the range suffices because everything is bounded (no
+// entry of X above |X|_2, about 1.2 for the usual coefficients).  X is held
+// times 2^12, A and B times 2^11, so that the small entries of large matrices
+// (1 / sqrt(m n) in X, 1 / m in A) stay normal numbers.  Rounding X costs most:
+// what it adds in weak directions grows by a in every step, to a share of the
+// result where U has few strong directions.  So X is held in two parts, high and
+// low (times 2^11), 22 bits together; the products read the high part, and the
+// sum a X takes both.  Against float64 the result is off by 0.9e-3 to 1.6e-3 of
+// its norm, below what rounding it to bf16 costs (1.7e-3); with the high part
+// alone a matrix of rank 1 was 15% off.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <utility>
+#include "ortho_kernels.h"
+
+namespace mx {
+
+namespace {
+
+typedef _Float16 half_t;
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kXcds = 8;
+constexpr int kRow = 128;                // bytes of an operand's row in one K step: 64 values
+constexpr float kScaleX = 0x1p12f, kScaleF = 0x1p11f, kLow = 0x1p11f;
+
+struct Args {
+  OrthoItem item[kOrthoGroup];
+  int end[kOrthoGroup];                  // workgroups of items 0 .. i
+  int count;
+};
+
+// A matrix as the kernels see it.
+struct View {
+  int m, n;                              // shorter and longer side, padded
+  double* parts;
+  half_t *x0, *x1, *low, *a, *b;         // x0 and x1 take turns
+};
+
+__device__ __forceinline__ View view(const OrthoItem& t) {
+  View v;
+  const int r = (t.rows + kOrthoPad - 1) / kOrthoPad * kOrthoPad, c = (t.cols + kOrthoPad - 1) / kOrthoPad * kOrthoPad;
+  v.m = min(r, c);
+  v.n = max(r, c);
+  v.parts = (double*)t.space;
+  v.x0 = (half_t*)(t.space + 8 * kOrthoParts);
+  const int64_t mn = (int64_t)v.m * v.n;
+  v.x1 = v.x0 + mn;
+  v.low = v.x1 + mn;
+  v.a = v.low + mn;
+  v.b = v.a + (int64_t)v.m * v.m;
+  return v;
+}
+
+// the item of a workgroup, and the workgroup's number in it
+__device__ __forceinline__ int find(const Args& a, int& id) {
+  int i = 0, base = 0;
+  while (i < a.count - 1 && (int)blockIdx.x >= a.end[i]) base = a.end[i++];
+  id = (int)blockIdx.x - base;
+  return i;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
+}
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// ---------------------------------------------------------------------------
+// The moment and the sum of squares: m = RN(RN(m mu) + RN(g (1 - mu))), and u =
+// RN(RN(g (1 - mu)) + RN(m mu)) (Nesterov) or m.  Squares are added in float64,
+// which no float32 overflows or sinks below.
+struct Moment {
+  float mu, rest, scale;                 // rest = 1 - mu
+  bool nesterov;
+};
+
+__device__ __forceinline__ float update_of(float g, float m, const Moment& c) {
+#pragma clang fp contract(off)
+  return c.nesterov ? g * c.rest + m * c.mu : m;
+}
+
+__device__ __forceinline__ float gradient(const OrthoItem& t, int64_t at) {
+  return t.g_bf16 ? bf16_value(((const uint16_t*)t.g)[at]) : ((const float*)t.g)[at];
+}
+
+__device__ __forceinline__ Moment moment_of(const OrthoStep& s) {
+  return Moment{s.momentum, s.rest, s.grad_scale ? *s.grad_scale : 1.0f, s.nesterov};
+}
+
+constexpr int kSumThreads = 1024;
+
+__global__ void __launch_bounds__(kSumThreads) ortho_sum(const Args a, const OrthoStep step) {
+#pragma clang fp contract(off)
+  __shared__ double red[kSumThreads / 64];
+  int id;
+  const OrthoItem& t = a.item[find(a, id)];
+  const View v = view(t);
+  const Moment c = moment_of(step);
+  const int64_t total = (int64_t)t.rows * t.cols, parts = min((int64_t)kOrthoParts, (total + kOrthoRun - 1) / kOrthoRun);
+  const int64_t each = (total + parts - 1) / parts, from = id * each, to = min(total, from + each);
+  double sum = 0.0;
+  for (int64_t at = from + threadIdx.x; at < to; at += kSumThreads) {
+    const int64_t row = at / t.cols, col = at - row * t.cols;
+    float u = gradient(t, row * t.ld_g + col) * c.scale;
+    if (t.moment != nullptr) {
+      const float m = t.moment[at] * c.mu + u * c.rest;
+      t.moment[at] = m;
+      u = update_of(u, m, c);
+    }
+    sum += (double)u * (double)u;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kSumThreads / 64; ++i) sum += red[i];
+    v.parts[id] = sum;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// X from U: a 64 x 64 piece of X a workgroup, zeros past U.  A tall U is
+// transposed through LDS.
+__global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep step) {
+  __shared__ double red[4];
+  __shared__ float piece[64][65];
+  int id;
+  const OrthoItem& t = a.item[find(a, id)];
+  const View v = view(t);
+  const Moment c = moment_of(step);
+  const int64_t total = (int64_t)t.rows * t.cols;
+  const int parts = (int)min((int64_t)kOrthoParts, (total + kOrthoRun - 1) / kOrthoRun);
+  double sum = (int)threadIdx.x < parts ? v.parts[threadIdx.x] : 0.0;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = (red[0] + red[1]) + (red[2] + red[3]);
+  const double scale = (double)kScaleX / (sqrt(sum) + step.eps);
+  const bool tall = t.rows > t.cols;
+  const int across = v.n / 64, m0 = id / across * 64, n0 = id % across * 64;
+  const int r0 = tall ? n0 : m0, c0 = tall ? m0 : n0;          // the piece in U
+  for (int i = threadIdx.x; i < 4096; i += 256) {
+    const int r = r0 + i / 64, k = c0 + i % 64;
+    float x = 0.0f;
+    if (r < t.rows && k < t.cols) {
+      const float g = gradient(t, (int64_t)r * t.ld_g + k) * c.scale;
+      const float u = t.moment != nullptr ? update_of(g, t.moment[(int64_t)r * t.cols + k], c) : g;
+      x = (float)((double)u * scale);
+    }
+    if (tall) piece[i % 64][i / 64] = x;
+    else piece[i / 64][i % 64] = x;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 4096; i += 256) {
+    const float x = piece[i / 64][i % 64];
+    const half_t hi = (half_t)x;
+    const int64_t at = (int64_t)(m0 + i / 64) * v.n + n0 + i % 64;
+    v.x0[at] = hi;
+    v.low[at] = (half_t)((x - (float)hi) * kLow);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The products: a workgroup of four waves takes a tile of the result, 64 F by 64
+// F, each wave a quarter of it, F x F fragments of the 32x32x16 instruction.
+// K advances 64 values (128 bytes of every row) a step, copied global -> LDS by
+// DMA into one of two stages while the other is consumed.
+//
+//   kGram  A = X X^T            both operands K-contiguous
+//   kPoly  B = b A + c A A      the same, A being its own transpose
+//   kStep  X' = a X + B X       the second operand has K as its rows: LDS reads
+//   kLast  O = B X              that transpose (ds_read_b64_tr_b16)
+//
+// A and B are symmetric: tiles on and below the diagonal are computed, and what
+// is below it is stored twice.
+//
+// Layout of the instruction: lane l holds row l % 32 of an operand and 8 of its
+// 16 k (8 (l / 32) ..); the 32 x 32 result has row 8 (r / 4) + 4 (l / 32) + r % 4 in
+// register r and column l % 32.  The columns of the product's tile are passed as
+// the instruction's rows, in an order that leaves a lane with sixteen
+// consecutive columns 16 (l / 32) .. of its row (strip_col).  For a tall
+// matrix's last step the two sides change places, so that the result leaves as
+// the rows of O's transpose.
+enum Mode { kGram, kPoly, kStep, kLast };
+
+// 16-byte piece's place in a 128-byte LDS row: a 16-byte LDS read serves the wave in groups of 16 lanes (0-3, 12-15 and
+// 20-27, and so on); with this order each group covers all 64 banks
+__device__ __forceinline__ int slot(int row, int piece) { return (piece ^ ((row >> 1) & 7)) * 16; }
+
+// the column that row f of a 32-column strip's fragment holds
+__device__ __forceinline__ int strip_col(int f) { return 16 * ((f >> 2) & 1) + 4 * (f >> 3) + (f & 3); }
+
+// Global -> LDS copy of 16 bytes per lane: LDS address = M0 + 16 * lane.  Inline asm, so that the compiler places no
+// waits of its own for it; it writes no register.  An SALU write of M0 needs one wait state before the copy reads it.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const T*)(((uint64_t)hi << 32) | lo);
+}
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(const F& f) {
+  each(std::make_integer_sequence<int, N>{}, f);
+}
+
+// what the last step writes: sixteen neighbouring results in row `row` of U's layout, from column `col`
+__device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rate, int row, int col, const float (&o)[16]) {
+  if (row >= t.rows || col >= t.cols) return;
+  const int left = t.cols - col;
+  if (t.w != nullptr) {
+    const int64_t at = (int64_t)row * t.cols + col;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e < left) {
+#pragma clang fp contract(off)
+        const float w = t.w[at + e] * keep - o[e] * rate;
+        t.w[at + e] = w;
+        if (t.copy != nullptr) t.copy[at + e] = (uint16_t)pack_bf16(w, 0.0f);
+      }
+    return;
+  }
+  const int64_t at = (int64_t)row * t.ld_out + col;
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (e < left) {
+      if (t.out_bf16) ((uint16_t*)t.out)[at + e] = (uint16_t)pack_bf16(o[e], 0.0f);
+      else ((float*)t.out)[at + e] = o[e];
+    }
+}
+
+struct Coef {
+  float a, b, c;
+  int from;                              // which X holds the step's
+  bool last;
+};
+
+template <int F, int MODE, bool TRANS>
+__global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args a, const OrthoStep step, const Coef c) {
+  constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  constexpr int T = 64 * F, kStage = T * kRow;
+  __shared__ __attribute__((aligned(1024))) uint8_t sP[2][kStage], sQ[2][kStage];
+  int id;
+  const OrthoItem& t = a.item[find(a, id)];
+  if (!kSym && MODE == kLast && (t.rows > t.cols) != TRANS) return;
+  const View v = view(t);
+  // An XCD (workgroup ids are dealt to them in turn, items start at a multiple of 8) takes a contiguous run of tiles.
+  const int tm = (v.m + T - 1) / T, tn = kSym ? tm : (v.n + T - 1) / T, tiles = kSym ? tm * (tm + 1) / 2 : tm * tn;
+  const int per = (tiles + kXcds - 1) / kXcds, tile = id % kXcds * per + id / kXcds;
+  if (id / kXcds >= per || tile >= tiles) return;
+  int ti, tj;
+  if constexpr (kSym) {
+    ti = (int)((sqrtf(8.0f * (float)tile + 1.0f) - 1.0f) * 0.5f);
+    while (ti * (ti + 1) / 2 > tile) --ti;
+    while ((ti + 1) * (ti + 2) / 2 <= tile) ++ti;
+    tj = tile - ti * (ti + 1) / 2;
+  } else {
+    // bands of four rows of tiles, column by column
+    const int band = tile / (4 * tn), in = tile % (4 * tn), rows = min(4, tm - 4 * band);
+    ti = 4 * band + in % rows;
+    tj = in / rows;
+  }
+  const int m0 = ti * T, n0 = tj * T;
+  const half_t* x = c.from ? v.x1 : v.x0;
+  const half_t* pp = MODE == kGram ? x : MODE == kPoly ? v.a : v.b;
+  const half_t* qq = MODE == kPoly ? v.a : x;
+  const int ldp = MODE == kGram ? v.n : v.m, ldq = MODE == kPoly ? v.m : v.n;
+  const int nk = (MODE == kGram ? v.n : v.m) / 64;
+
+  const int th = threadIdx.x, lane = th & 63, wave = __builtin_amdgcn_readfirstlane(th >> 6);
+  const int wm = 32 * F * (wave & 1), wn = 32 * F * (wave >> 1);
+  const int l32 = lane & 31, h = lane >> 5;
+
+  // Copies: one instruction moves 1 KB, eight LDS rows of a K-contiguous operand or a run of the other's rows; a wave
+  // copies a quarter of each operand.  Rows and columns past the padded size read the last ones again.
+  constexpr int kCopies = 2 * F;
+  uint32_t op[kCopies], oq[kCopies];
+#pragma unroll
+  for (int e = 0; e < kCopies; ++e) {
+    const int f = (wave * kCopies + e) * 8 + (lane >> 3);
+    const int pr = TRANS ? (f & ~31) + strip_col(f & 31) : f;
+    op[e] = (uint32_t)min(pr, v.m - 1 - m0) * (uint32_t)(2 * ldp) + (uint32_t)(((lane & 7) ^ ((f >> 1) & 7)) * 16);
+    if constexpr (kSym) {
+      const int qr = (f & ~31) + strip_col(f & 31);
+      oq[e] = (uint32_t)min(qr, v.m - 1 - n0) * (uint32_t)(2 * ldq) + (uint32_t)(((lane & 7) ^ ((f >> 1) & 7)) * 16);
+    } else {
+      // K row k of T values, its 64-byte pieces in an order that parts four neighbouring rows' banks
+      const int at = (wave * kCopies + e) * 1024 + lane * 16, k = at / (2 * T), piece = at % (2 * T) / 16;
+      const int turn = F == 1 ? (k >> 1) & 1 : k & 3;
+      const int col = 8 * ((((piece >> 2) ^ turn) << 2) + (piece & 3));
+      oq[e] = (uint32_t)k * (uint32_t)(2 * ldq) + (uint32_t)(2 * min(col, v.n - 8 - n0));
+    }
+  }
+  const uint8_t* cp = uniform((const uint8_t*)(pp + (int64_t)m0 * ldp));
+  const uint8_t* cq = uniform((const uint8_t*)(kSym ? qq + (int64_t)n0 * ldq : qq + n0));
+  const int64_t stepq = kSym ? kRow : (int64_t)128 * ldq;          // 64 values, or 64 rows
+  const uint32_t dP = lds_addr(&sP[0][wave * kCopies * 1024]), dQ = lds_addr(&sQ[0][wave * kCopies * 1024]);
+  auto copy = [&](int st, int e) {
+    dma16(cp, op[e], dP + st * kStage + e * 1024);
+    dma16(cq, oq[e], dQ + st * kStage + e * 1024);
+  };
+  auto advance = [&]() {
+    cp += kRow;
+    cq += stepq;
+  };
+
+  // a fragment's place in LDS: rows 32 apart are immediates, the four K parts of a step turn the pieces
+  uint32_t rp[4], rq[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) rp[s] = (uint32_t)((wm + l32) * kRow + slot(l32, 2 * s + h));
+  const int chunk = 4 * ((lane >> 4) & 1) + (lane & 3), krow = 8 * h + ((lane >> 2) & 3);
+  if constexpr (kSym) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) rq[s] = (uint32_t)((wn + l32) * kRow + slot(l32, 2 * s + h));
+  } else {
+    // strip j of the wave: chunk `chunk` of four columns (in fragment order) of K row krow; 4, 8, 12 .. rows on are
+    // immediates
+    const int col = TRANS ? 4 * chunk : strip_col(4 * chunk);
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+      const int seg = (wn >> 5) + j, turn = F == 1 ? (krow >> 1) & 1 : krow & 3;
+      rq[j] = (uint32_t)(krow * 2 * T + (seg ^ turn) * 64 + col * 2);
+    }
+  }
+  auto read_p = [&](int st, int s, int i) { return *(const v8h*)(sP[st] + rp[s] + i * 32 * kRow); };
+  auto read_q = [&](int st, int s, int j) {
+    if constexpr (kSym) {
+      return *(const v8h*)(sQ[st] + rq[s] + j * 32 * kRow);
+    } else {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4s lds_v4s;
+      const uint8_t* p = sQ[st] + rq[j] + s * 16 * 2 * T;
+      const v4h lo = __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p));
+      const v4h hi = __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * T)));
+      return v8h{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+  };
+
+  v16f acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+#pragma unroll
+  for (int e = 0; e < kCopies; ++e) copy(0, e);
+  advance();
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  if (nk > 1) {
+#pragma unroll
+    for (int e = 0; e < kCopies; ++e) copy(1, e);
+    advance();
+  }
+  v8h fp[2][F], fq[2][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i) {
+    fp[0][i] = read_p(0, 0, i);
+    fq[0][i] = read_q(0, 0, i);
+  }
+  int st = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    const bool more = kt + 1 < nk, issue = kt + 2 < nk;
+    each<4>([&](auto part) {
+      constexpr int s = decltype(part)::value, now = s & 1, next = now ^ 1;
+      if constexpr (s == 3) {
+        // every read of this stage is done, and the next one has landed
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      }
+      each<F * F>([&](auto index) {
+        constexpr int n = decltype(index)::value, i = n / F, j = n % F;
+        if constexpr (s < 3) {
+          if constexpr (n < F) {
+            fp[next][n] = read_p(st, s + 1, n);
+            fq[next][n] = read_q(st, s + 1, n);
+          }
+        } else {
+          if constexpr (n < F) {
+            if (more) {
+              fp[next][n] = read_p(st ^ 1, 0, n);
+              fq[next][n] = read_q(st ^ 1, 0, n);
+            }
+          }
+        }
+        acc[i][j] = TRANS ? __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[now][i], fq[now][j], acc[i][j], 0, 0, 0)
+                          : __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[now][j], fp[now][i], acc[i][j], 0, 0, 0);
+        if constexpr (s == 3) {
+          constexpr int per = (kCopies + F * F - 1) / (F * F);
+          if (issue) {
+#pragma unroll
+            for (int e = n * per; e < (n + 1) * per; ++e)
+              if (e < kCopies) copy(st, e);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (s == 3) {
+        if (issue) advance();
+      }
+    });
+    st ^= 1;
+  }
+
+  float keep = 1.0f, rate = 0.0f;
+  if constexpr (MODE == kLast) {
+    if (t.w != nullptr) {
+      const double lr = step.lr_dev ? (double)*step.lr_dev : step.lr;
+      keep = (float)(1.0 - lr * step.weight_decay);
+      rate = (float)(lr * t.scale);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+      // TRANS: the lane's column is l % 32 of strip j, its rows 16 h .. of strip i
+      const int m = m0 + wm + 32 * i + (TRANS ? 16 * h : l32), n = n0 + wn + 32 * j + (TRANS ? l32 : 16 * h);
+      if (m >= v.m || n >= (kSym ? v.m : v.n)) continue;
+      const v16f d = acc[i][j];
+      if constexpr (MODE == kLast) {
+        float o[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[r] = d[r] * (1.0f / (kScaleX * kScaleF));
+        if constexpr (TRANS) finish(t, keep, rate, n, m, o);
+        else finish(t, keep, rate, m, n, o);
+      } else if constexpr (kSym) {
+        float o[16];
+        if constexpr (MODE == kGram) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] = d[r] * (kScaleF / (kScaleX * kScaleX));
+        } else {
+          const v8h* base = (const v8h*)(v.a + (int64_t)m * v.m + n);
+          const v8h b0 = base[0], b1 = base[1];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            o[r] = fmaf(c.b, (float)(r < 8 ? b0[r & 7] : b1[r & 7]), d[r] * (c.c / kScaleF));
+            if (c.last && n + r == m) o[r] += c.a * kScaleF;
+          }
+        }
+        half_t* out = MODE == kGram ? v.a : v.b;
+        v8h w0, w1;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          w0[r] = (half_t)o[r];
+          w1[r] = (half_t)o[8 + r];
+        }
+        v8h* to = (v8h*)(out + (int64_t)m * v.m + n);
+        to[0] = w0;
+        to[1] = w1;
+        if (ti != tj) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) out[(int64_t)(n + r) * v.m + m] = r < 8 ? w0[r & 7] : w1[r & 7];
+        }
+      } else {
+        const int64_t at = (int64_t)m * v.n + n;
+        const v8h* hi = (const v8h*)(x + at);
+        v8h* lo = (v8h*)(v.low + at);
+        v8h* to = (v8h*)((c.from ? v.x0 : v.x1) + at);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const v8h xh = hi[q], xl = lo[q];
+          v8h nh, nl;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float y = fmaf(c.a, fmaf((float)xl[r], 1.0f / kLow, (float)xh[r]), d[8 * q + r] * (1.0f / kScaleF));
+            nh[r] = (half_t)y;
+            nl[r] = (half_t)((y - (float)nh[r]) * kLow);
+          }
+          to[q] = nh;
+          lo[q] = nl;
+        }
+      }
+    }
+}
+
+// Workgroups of each item, `of(item)` of them, as a's table; their number.
+template <typename Of>
+int deal(Args& a, const Of& of) {
+  int total = 0;
+  for (int i = 0; i < kOrthoGroup; ++i) {
+    if (i < a.count) total += of(a.item[i]);
+    a.end[i] = total;
+  }
+  return total;
+}
+
+template <int F, int MODE>
+void products(Args& a, const OrthoStep& step, const Coef& c, hipStream_t s) {
+  constexpr int T = 64 * F;
+  const int total = deal(a, [&](const OrthoItem& t) {
+    const OrthoSize z = ortho_size(t.rows, t.cols);
+    const int64_t tm = (z.m + T - 1) / T, tn = (z.n + T - 1) / T;
+    const int64_t tiles = MODE == kGram || MODE == kPoly ? tm * (tm + 1) / 2 : tm * tn;
+    return (int)((tiles + kXcds - 1) / kXcds * kXcds);
+  });
+  bool wide = MODE != kLast, tall = false;
+  if (MODE == kLast)
+    for (int i = 0; i < a.count; ++i) (a.item[i].rows > a.item[i].cols ? tall : wide) = true;
+  if (wide) hipLaunchKernelGGL((ortho_product<F, MODE, false>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
+  if constexpr (MODE == kLast) {
+    if (tall) hipLaunchKernelGGL((ortho_product<F, MODE, true>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
+  }
+}
+
+template <int MODE>
+void products_of(Args& a, int f, const OrthoStep& step, const Coef& c, hipStream_t s) {
+  if (f == 4) products<4, MODE>(a, step, c, s);
+  else if (f == 2) products<2, MODE>(a, step, c, s);
+  else products<1, MODE>(a, step, c, s);
+}
+
+}  // namespace
+
+hipError_t launch_ortho(const OrthoItem* items, int count, const OrthoStep& step, hipStream_t s) {
+  Args a;
+  a.count = count;
+  for (int i = 0; i < kOrthoGroup; ++i) a.item[i] = items[i < count ? i : count - 1];
+  int total = deal(a, [](const OrthoItem& t) { return (int)ortho_size(t.rows, t.cols).parts; });
+  hipLaunchKernelGGL(ortho_sum, dim3((unsigned)total), dim3(kSumThreads), 0, s, a, step);
+  total = deal(a, [](const OrthoItem& t) {
+    const OrthoSize z = ortho_size(t.rows, t.cols);
+    return (int)(z.m / 64 * (z.n / 64));
+  });
+  hipLaunchKernelGGL(ortho_start, dim3((unsigned)total), dim3(256), 0, s, a, step);
+  int64_t large = 0;
+  for (int i = 0; i < count; ++i) {
+    const OrthoSize z = ortho_size(a.item[i].rows, a.item[i].cols);
+    large += z.m * z.n;
+  }
+  const int f = large >= (int64_t)1 << 22 ? 4 : large >= (int64_t)1 << 18 ? 2 : 1;
+  Coef c{(float)step.a, (float)step.b, (float)step.c, 0, false};
+  for (int k = 0; k < step.steps; ++k) {
+    c.last = k + 1 == step.steps;
+    c.from = k & 1;
+    products_of<kGram>(a, f, step, c, s);
+    products_of<kPoly>(a, f, step, c, s);
+    if (c.last) products_of<kLast>(a, f, step, c, s);
+    else products_of<kStep>(a, f, step, c, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -1,0 +1,112 @@
+// How a list of matrices is orthogonalized: the sizes of what is held of each,
+// the bounds of the iteration, and the tiles of its products.  Host-only logic,
+// no HIP types, so that it can be compiled and checked on a machine without a
+// GPU.
+#pragma once
+#include <math.h>
+#include <stdint.h>
+
+namespace mx {
+
+constexpr int kOrthoGroup = 32;                    // matrices in one launch's arguments
+constexpr int kOrthoPad = 64;                      // sizes are padded to this: one K step of the products
+constexpr int64_t kOrthoSide = int64_t(1) << 20;   // rows and columns stay below
+constexpr int64_t kOrthoMinor = int64_t(1) << 16;  // the shorter side too
+constexpr int kOrthoParts = 256;                   // sums of squares of a matrix at most
+constexpr int64_t kOrthoRun = 8192;                // elements for each of them at least
+
+inline int64_t ortho_pad(int64_t n) { return (n + kOrthoPad - 1) / kOrthoPad * kOrthoPad; }
+
+// A matrix's place in the workspace, in bytes: the sums of squares (float64), then X, the next X and X's low part
+// [m][n], A and B [m][m] in float16; m the shorter side, n the longer, both padded.
+struct OrthoSize {
+  int64_t m, n;                                    // padded
+  int64_t parts;                                   // sums of squares
+  int64_t bytes;
+};
+
+inline OrthoSize ortho_size(int64_t rows, int64_t cols) {
+  OrthoSize s;
+  s.m = ortho_pad(rows < cols ? rows : cols);
+  s.n = ortho_pad(rows < cols ? cols : rows);
+  s.parts = (rows * cols + kOrthoRun - 1) / kOrthoRun;
+  if (s.parts > kOrthoParts) s.parts = kOrthoParts;
+  s.bytes = 8 * kOrthoParts + 2 * (3 * s.m * s.n + 2 * s.m * s.m);
+  return s;
+}
+
+// Matrices that are worked on together: as many of the list's next ones as one launch's arguments hold and as stay
+// within this many bytes of workspace (one matrix at least).  2 GiB hold the linears of a large block, whose products
+// fill the chip many times over.
+constexpr int64_t kOrthoBytes = int64_t(2) << 30;
+
+// visit(indexes, their number, bytes) for each group of a list whose entries have rows and cols, until it returns
+// false; empty entries are in none.
+template <typename T, typename Visit>
+inline void each_ortho_group(const T* list, int32_t count, const Visit& visit) {
+  int32_t at[kOrthoGroup];
+  int n = 0;
+  int64_t bytes = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (list[i].rows == 0 || list[i].cols == 0) continue;
+    const int64_t next = ortho_size(list[i].rows, list[i].cols).bytes;
+    if (n > 0 && (n == kOrthoGroup || bytes + next > kOrthoBytes)) {
+      if (!visit(at, n, bytes)) return;
+      n = 0;
+      bytes = 0;
+    }
+    at[n++] = i;
+    bytes += next;
+  }
+  if (n > 0) visit(at, n, bytes);
+}
+
+// The largest |p(s)|, p(s) = a s + b s^3 + c s^5, for 0 <= s <= top, and the largest |b t + c t^2| and |a + b t + c t^2|
+// for 0 <= t <= top^2: what bounds X, and the factors that multiply it, in the next step.
+struct OrthoReach {
+  double x, factor;
+};
+
+inline OrthoReach ortho_reach(double a, double b, double c, double top) {
+  OrthoReach r = {0.0, 0.0};
+  const double end = top * top;
+  auto at = [&](double t) {                        // t = s^2
+    if (!(t >= 0.0 && t <= end)) return;
+    const double x = fabs(sqrt(t) * (a + t * (b + t * c))), f = fabs(t * (b + t * c)), q = fabs(a + t * (b + t * c));
+    r.x = fmax(r.x, x);
+    r.factor = fmax(r.factor, fmax(f, q));
+  };
+  at(0.0);
+  at(end);
+  if (c != 0.0) at(-b / (2.0 * c));
+  // p'(s) = a + 3 b t + 5 c t^2
+  if (c != 0.0) {
+    const double d = 9.0 * b * b - 20.0 * a * c;
+    if (d >= 0.0) {
+      at((-3.0 * b + sqrt(d)) / (10.0 * c));
+      at((-3.0 * b - sqrt(d)) / (10.0 * c));
+    }
+  } else if (b != 0.0) {
+    at(-a / (3.0 * b));
+  }
+  return r;
+}
+
+// Whether X (held times 2^12) and its factors (times 2^11) stay within float16 through all steps, with half of its
+// range to spare: singular values start at 1 or below.
+constexpr double kOrthoMostX = 4.0, kOrthoMostFactor = 15.0;
+
+inline bool ortho_fits(double a, double b, double c, int steps) {
+  if (!isfinite(a) || !isfinite(b) || !isfinite(c)) return false;
+  double top = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    const OrthoReach r = ortho_reach(a, b, c, top);
+    if (!(r.x <= kOrthoMostX && r.factor <= kOrthoMostFactor)) return false;
+    if (top * top > kOrthoMostFactor) return false;            // A itself
+    if (i > 0 && r.x <= top) break;                            // from here on the bound does not grow
+    top = r.x > top ? r.x : top;
+  }
+  return true;
+}
+
+}  // namespace mx

@@ -554,6 +554,104 @@ mx_status mx_layer_norm_grad(const void *dy, int64_t ld_dy, const void *x, int64
  * type that it refuses). */
 int64_t mx_layer_norm_grad_workspace(int64_t rows, int64_t cols, mx_out type, int32_t sums);
 
+/*
+ * Orthogonalized updates.  From X = G / (|G| + eps), |.| the Frobenius norm,
+ * `steps` Newton-Schulz steps
+ *   X <- a X + (b A + c A A) X,   A = X X^T
+ * turn each singular value s of X into a s + b s^3 + c s^5, step by step, and
+ * leave its singular vectors: with a = 3.4445, b = -4.7750, c = 2.0315 and five
+ * steps all but the weakest end between 0.68 and 1.13.
+ * The products take float16 operands (X times 2^12, A and B times 2^11) and sum
+ * in float32; X is carried from step to step as two float16 parts, 22 bits.  The
+ * result is off by up to about 2e-3 of its norm before it is rounded.  A matrix
+ * that holds Inf or NaN becomes NaN; one of zeros stays zero.
+ */
+typedef struct {
+  double a, b, c;     /* such that X and its factors stay small from singular
+                         values of at most 1 on: |p(s)| <= 4, and b t + c t^2
+                         and a + b t + c t^2 within 15, t = s^2; others are
+                         rejected */
+  double eps;         /* finite, > 0 */
+  int32_t steps;      /* 1 .. 64 */
+} mx_ortho_params;
+
+/*
+ * mx_orthogonalize: out = the steps' X, for each matrix of a list.
+ *   matrices   host array of count entries, read before the call returns; any
+ *              count; entries with rows or cols 0 are skipped; rows and cols <
+ *              2^20, the smaller of them < 2^16
+ *   g, out     device, row-major, aligned to their element, ld_g and ld_out
+ *              elements between rows, >= cols; no out may overlap another, a g
+ *              of any entry or the workspace
+ *   workspace  16-byte aligned device memory of at least
+ *              mx_orthogonalize_workspace bytes, this call's alone until it has
+ *              run; it needs no initial value
+ * The list's matrices are worked on together, up to 32 at a time.  A matrix's
+ * result depends on the matrix, the parameters and the sizes of those that it
+ * is worked on with, never on timing.
+ */
+typedef struct {
+  const void *g;
+  void *out;
+  int64_t rows, cols, ld_g, ld_out;
+  mx_out grad, type;  /* of g and of out: MX_OUT_F32 or MX_OUT_BF16 */
+} mx_ortho_matrix;
+
+mx_status mx_orthogonalize(const mx_ortho_matrix *matrices, int32_t count, const mx_ortho_params *params,
+                           void *workspace, int64_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace that mx_orthogonalize needs for matrices of these sizes (0 also for ones that it refuses). */
+int64_t mx_orthogonalize_workspace(const mx_ortho_matrix *matrices, int32_t count);
+
+/*
+ * mx_muon_step: one Muon step over a list of float32 weight matrices; vectors
+ * and tables take mx_adamw_step.  Per matrix, in float32 with one rounding per
+ * operation outside the orthogonalization:
+ *   g = g * grad_scale                                (if one is given)
+ *   m = m * momentum + g * (1 - momentum)
+ *   u = g * (1 - momentum) + m * momentum             (nesterov), or m
+ *   o = u orthogonalized, as above
+ *   w = w * (1 - lr * weight_decay) - o * (lr * adjust)
+ *   copy = w as bf16, to nearest even                 (if one is given)
+ *   adjust     MX_MUON_RMS: 0.2 sqrt(max(rows, cols)), so that an update has the
+ *              size of an AdamW update; MX_MUON_SHAPE: sqrt(max(1, rows / cols));
+ *              MX_MUON_PLAIN: 1
+ *   tensors    as the matrices above; w, g, m, copy are contiguous [rows][cols];
+ *              what the step writes (w, m, copy) must overlap no other array of
+ *              any entry (gradients may be shared), nor the workspace, nor the
+ *              device's lr and grad_scale
+ *   momentum   0 <= momentum < 1
+ *   lr_dev     if not NULL, the device's float32 is read instead of lr when the
+ *              kernel runs, so that a captured graph replays with a rate that
+ *              moves on
+ *   grad_scale NULL, or a device float32 (the clipping or loss-scale factor)
+ */
+typedef enum { MX_MUON_PLAIN = 0, MX_MUON_RMS = 1, MX_MUON_SHAPE = 2 } mx_muon_adjust;
+
+typedef struct {
+  float *w;
+  const void *g;      /* float32 or bf16, by grad */
+  float *m;
+  uint16_t *copy;     /* bf16 bit patterns, or NULL */
+  int64_t rows, cols;
+  mx_out grad;
+} mx_muon_tensor;
+
+typedef struct {
+  mx_ortho_params ortho;
+  double lr, momentum, weight_decay;
+  int32_t nesterov;   /* 0 or 1 */
+  mx_muon_adjust adjust;
+  const float *lr_dev;
+  const float *grad_scale;
+} mx_muon_params;
+
+mx_status mx_muon_step(const mx_muon_tensor *tensors, int32_t count, const mx_muon_params *params, void *workspace,
+                       int64_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace that mx_muon_step needs for tensors of these sizes (0 also for ones that it refuses). */
+int64_t mx_muon_workspace(const mx_muon_tensor *tensors, int32_t count);
+
 /* A static, human-readable name for a status code. */
 const char *mx_status_str(mx_status status);
 

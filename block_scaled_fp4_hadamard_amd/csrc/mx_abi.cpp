@@ -647,6 +647,7 @@ mx_status mx_orthogonalize(const mx_ortho_matrix* matrices, int32_t count, const
     if (t.rows == 0 || t.cols == 0) continue;
     if (!norm_rows_ok(t.g, t.grad, t.ld_g, t.cols) || !norm_rows_ok(t.out, t.type, t.ld_out, t.cols))
       return MX_ERR_INVALID;
+    if (t.ld_out >= mx::kOrthoPitch) return MX_ERR_INVALID;
   }
   const int64_t need = ortho_workspace(matrices, count);
   if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)) return MX_ERR_INVALID;

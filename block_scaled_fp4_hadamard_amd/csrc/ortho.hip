@@ -49,7 +49,8 @@ struct Args {
 
 // A matrix as the kernels see it.
 struct View {
-  int m, n;                              // shorter and longer side, padded
+  int m, n;                              // shorter and longer side, in whole K steps
+  int lm, ln;                            // and with room for any tile's rest
   double* parts;
   half_t *x0, *x1, *low, *a, *b;         // x0 and x1 take turns
 };
@@ -59,13 +60,15 @@ __device__ __forceinline__ View view(const OrthoItem& t) {
   const int r = (t.rows + kOrthoPad - 1) / kOrthoPad * kOrthoPad, c = (t.cols + kOrthoPad - 1) / kOrthoPad * kOrthoPad;
   v.m = min(r, c);
   v.n = max(r, c);
+  v.lm = v.m + kOrthoRest;
+  v.ln = v.n + kOrthoRest;
   v.parts = (double*)t.space;
   v.x0 = (half_t*)(t.space + 8 * kOrthoParts);
-  const int64_t mn = (int64_t)v.m * v.n;
+  const int64_t mn = (int64_t)v.lm * v.ln;
   v.x1 = v.x0 + mn;
   v.low = v.x1 + mn;
   v.a = v.low + mn;
-  v.b = v.a + (int64_t)v.m * v.m;
+  v.b = v.a + (int64_t)v.lm * v.lm;
   return v;
 }
 
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kSumThreads) ortho_sum(const Args a, const Ort
 #pragma clang fp contract(off)
   __shared__ double red[kSumThreads / 64];
   int id;
-  const OrthoItem& t = a.item[find(a, id)];
+  const OrthoItem t = a.item[find(a, id)];
   const View v = view(t);
   const Moment c = moment_of(step);
   const int64_t total = (int64_t)t.rows * t.cols, parts = min((int64_t)kOrthoParts, (total + kOrthoRun - 1) / kOrthoRun);
@@ -137,13 +140,13 @@ __global__ void __launch_bounds__(kSumThreads) ortho_sum(const Args a, const Ort
 }
 
 // ---------------------------------------------------------------------------
-// X from U: a 64 x 64 piece of X a workgroup, zeros past U.  A tall U is
-// transposed through LDS.
+// X from U: a 64 x 64 piece of X a workgroup, zeros up to whole K steps.  A tall
+// U is transposed through LDS.
 __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep step) {
   __shared__ double red[4];
   __shared__ float piece[64][65];
   int id;
-  const OrthoItem& t = a.item[find(a, id)];
+  const OrthoItem t = a.item[find(a, id)];
   const View v = view(t);
   const Moment c = moment_of(step);
   const int64_t total = (int64_t)t.rows * t.cols;
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
   for (int i = threadIdx.x; i < 4096; i += 256) {
     const float x = piece[i / 64][i % 64];
     const half_t hi = (half_t)x;
-    const int64_t at = (int64_t)(m0 + i / 64) * v.n + n0 + i % 64;
+    const int64_t at = (int64_t)(m0 + i / 64) * v.ln + n0 + i % 64;
     v.x0[at] = hi;
     v.low[at] = (half_t)((x - (float)hi) * kLow);
   }
@@ -196,10 +199,10 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 // Layout of the instruction: lane l holds row l % 32 of an operand and 8 of its
 // 16 k (8 (l / 32) ..); the 32 x 32 result has row 8 (r / 4) + 4 (l / 32) + r % 4 in
 // register r and column l % 32.  The columns of the product's tile are passed as
-// the instruction's rows, in an order that leaves a lane with sixteen
-// consecutive columns 16 (l / 32) .. of its row (strip_col).  For a tall
-// matrix's last step the two sides change places, so that the result leaves as
-// the rows of O's transpose.
+// the instruction's rows, in an order that leaves a lane with columns 8 (l / 32)
+// .. + 7 and 16 more of its row (strip_col), so that a wave's 16-byte accesses
+// meet 32 bytes of each row.  For a tall matrix's last step the two sides change
+// places, so that the result leaves as the rows of O's transpose.
 enum Mode { kGram, kPoly, kStep, kLast };
 
 // 16-byte piece's place in a 128-byte LDS row: a 16-byte LDS read serves the wave in groups of 16 lanes (0-3, 12-15 and
@@ -207,7 +210,9 @@ enum Mode { kGram, kPoly, kStep, kLast };
 __device__ __forceinline__ int slot(int row, int piece) { return (piece ^ ((row >> 1) & 7)) * 16; }
 
 // the column that row f of a 32-column strip's fragment holds
-__device__ __forceinline__ int strip_col(int f) { return 16 * ((f >> 2) & 1) + 4 * (f >> 3) + (f & 3); }
+__device__ __forceinline__ int strip_col(int f) {
+  return 16 * (f >> 4) + 8 * ((f >> 2) & 1) + 4 * ((f >> 3) & 1) + (f & 3);
+}
 
 // Global -> LDS copy of 16 bytes per lane: LDS address = M0 + 16 * lane.  Inline asm, so that the compiler places no
 // waits of its own for it; it writes no register.  An SALU write of M0 needs one wait state before the copy reads it.
@@ -218,11 +223,11 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 template <typename T>
-__device__ __forceinline__ const T* uniform(const T* p) {
+__device__ __forceinline__ T* uniform(T* p) {
   const uint64_t v = (uint64_t)p;
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const T*)(((uint64_t)hi << 32) | lo);
+  return (T*)(((uint64_t)hi << 32) | lo);
 }
 template <int... I, typename F>
 __device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& f) {
@@ -233,29 +238,59 @@ __device__ __forceinline__ void each(const F& f) {
   each(std::make_integer_sequence<int, N>{}, f);
 }
 
-// what the last step writes: sixteen neighbouring results in row `row` of U's layout, from column `col`
-__device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rate, int row, int col, const float (&o)[16]) {
+// 16 bytes wherever a row may start: one access, whatever the row pitch and the width
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// What the last step writes: eight neighbouring results in row `row` of U's layout, from column `col`, the lane's `own`
+// elements on from the wave's element `first`.  `w`: the weights there, read ahead where all eight exist.
+__device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rate, int row, int col, int64_t first,
+                                       uint32_t own, const float (&o)[8], const u32x4 (&w)[2]) {
+#pragma clang fp contract(off)
   if (row >= t.rows || col >= t.cols) return;
   const int left = t.cols - col;
+  float y[8];
   if (t.w != nullptr) {
-    const int64_t at = (int64_t)row * t.cols + col;
+    float* to = uniform(t.w + first) + own;
+    uint16_t* copy = uniform(t.copy + first) + own;
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (e < left) {
-#pragma clang fp contract(off)
-        const float w = t.w[at + e] * keep - o[e] * rate;
-        t.w[at + e] = w;
-        if (t.copy != nullptr) t.copy[at + e] = (uint16_t)pack_bf16(w, 0.0f);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float old = left >= 8 ? __uint_as_float(w[e >> 2][e & 3]) : e < left ? to[e] : 0.0f;
+      y[e] = old * keep - o[e] * rate;
+    }
+    const u32x4 h = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+    if (left >= 8) {
+      ((u32x4_any*)to)[0] = u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
+      ((u32x4_any*)to)[1] = u32x4{__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])};
+      if (t.copy != nullptr) *(u32x4_any*)copy = h;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) {
+          to[e] = y[e];
+          if (t.copy != nullptr) copy[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+        }
+    }
     return;
   }
-  const int64_t at = (int64_t)row * t.ld_out + col;
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e < left) {
-      if (t.out_bf16) ((uint16_t*)t.out)[at + e] = (uint16_t)pack_bf16(o[e], 0.0f);
-      else ((float*)t.out)[at + e] = o[e];
+  uint16_t* out16 = uniform((uint16_t*)t.out + first) + own;
+  float* out32 = uniform((float*)t.out + first) + own;
+  const u32x4 h = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])};
+  if (left >= 8) {
+    if (t.out_bf16) {
+      *(u32x4_any*)out16 = h;
+    } else {
+      u32x4_any* to = (u32x4_any*)out32;
+      to[0] = u32x4{__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])};
+      to[1] = u32x4{__float_as_uint(o[4]), __float_as_uint(o[5]), __float_as_uint(o[6]), __float_as_uint(o[7])};
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) {
+        if (t.out_bf16) out16[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+        else out32[e] = o[e];
+      }
+  }
 }
 
 struct Coef {
@@ -270,7 +305,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
   constexpr int T = 64 * F, kStage = T * kRow;
   __shared__ __attribute__((aligned(1024))) uint8_t sP[2][kStage], sQ[2][kStage];
   int id;
-  const OrthoItem& t = a.item[find(a, id)];
+  const OrthoItem t = a.item[find(a, id)];
   if (!kSym && MODE == kLast && (t.rows > t.cols) != TRANS) return;
   const View v = view(t);
   // An XCD (workgroup ids are dealt to them in turn, items start at a multiple of 8) takes a contiguous run of tiles.
@@ -293,7 +328,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
   const half_t* x = c.from ? v.x1 : v.x0;
   const half_t* pp = MODE == kGram ? x : MODE == kPoly ? v.a : v.b;
   const half_t* qq = MODE == kPoly ? v.a : x;
-  const int ldp = MODE == kGram ? v.n : v.m, ldq = MODE == kPoly ? v.m : v.n;
+  const int ldp = MODE == kGram ? v.ln : v.lm, ldq = MODE == kPoly ? v.lm : v.ln;
   const int nk = (MODE == kGram ? v.n : v.m) / 64;
 
   const int th = threadIdx.x, lane = th & 63, wave = __builtin_amdgcn_readfirstlane(th >> 6);
@@ -301,34 +336,35 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
   const int l32 = lane & 31, h = lane >> 5;
 
   // Copies: one instruction moves 1 KB, eight LDS rows of a K-contiguous operand or a run of the other's rows; a wave
-  // copies a quarter of each operand.  Rows and columns past the padded size read the last ones again.
+  // copies a quarter of each operand.  Rows and columns past the matrix hold anything: each spoils its own row or column of
+  // the result, which lies past the matrix too.
   constexpr int kCopies = 2 * F;
   uint32_t op[kCopies], oq[kCopies];
 #pragma unroll
   for (int e = 0; e < kCopies; ++e) {
     const int f = (wave * kCopies + e) * 8 + (lane >> 3);
     const int pr = TRANS ? (f & ~31) + strip_col(f & 31) : f;
-    op[e] = (uint32_t)min(pr, v.m - 1 - m0) * (uint32_t)(2 * ldp) + (uint32_t)(((lane & 7) ^ ((f >> 1) & 7)) * 16);
+    op[e] = (uint32_t)pr * (uint32_t)(2 * ldp) + (uint32_t)(((lane & 7) ^ ((f >> 1) & 7)) * 16);
     if constexpr (kSym) {
       const int qr = (f & ~31) + strip_col(f & 31);
-      oq[e] = (uint32_t)min(qr, v.m - 1 - n0) * (uint32_t)(2 * ldq) + (uint32_t)(((lane & 7) ^ ((f >> 1) & 7)) * 16);
+      oq[e] = (uint32_t)qr * (uint32_t)(2 * ldq) + (uint32_t)(((lane & 7) ^ ((f >> 1) & 7)) * 16);
     } else {
       // K row k of T values, its 64-byte pieces in an order that parts four neighbouring rows' banks
       const int at = (wave * kCopies + e) * 1024 + lane * 16, k = at / (2 * T), piece = at % (2 * T) / 16;
       const int turn = F == 1 ? (k >> 1) & 1 : k & 3;
       const int col = 8 * ((((piece >> 2) ^ turn) << 2) + (piece & 3));
-      oq[e] = (uint32_t)k * (uint32_t)(2 * ldq) + (uint32_t)(2 * min(col, v.n - 8 - n0));
+      oq[e] = (uint32_t)k * (uint32_t)(2 * ldq) + (uint32_t)(2 * col);
     }
   }
   const uint8_t* cp = uniform((const uint8_t*)(pp + (int64_t)m0 * ldp));
   const uint8_t* cq = uniform((const uint8_t*)(kSym ? qq + (int64_t)n0 * ldq : qq + n0));
   const int64_t stepq = kSym ? kRow : (int64_t)128 * ldq;          // 64 values, or 64 rows
   const uint32_t dP = lds_addr(&sP[0][wave * kCopies * 1024]), dQ = lds_addr(&sQ[0][wave * kCopies * 1024]);
-  auto copy = [&](int st, int e) {
-    dma16(cp, op[e], dP + st * kStage + e * 1024);
-    dma16(cq, oq[e], dQ + st * kStage + e * 1024);
+  auto copy = [&](int st, int n) __attribute__((always_inline)) {
+    if (n & 1) dma16(cq, oq[n >> 1], dQ + st * kStage + (n >> 1) * 1024);
+    else dma16(cp, op[n >> 1], dP + st * kStage + (n >> 1) * 1024);
   };
-  auto advance = [&]() {
+  auto advance = [&]() __attribute__((always_inline)) {
     cp += kRow;
     cq += stepq;
   };
@@ -342,7 +378,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
 #pragma unroll
     for (int s = 0; s < 4; ++s) rq[s] = (uint32_t)((wn + l32) * kRow + slot(l32, 2 * s + h));
   } else {
-    // strip j of the wave: chunk `chunk` of four columns (in fragment order) of K row krow; 4, 8, 12 .. rows on are
+    // strip j of the wave: chunk `chunk` of four columns (in fragment order) of K row krow; rows 4, 16 .. on are
     // immediates
     const int col = TRANS ? 4 * chunk : strip_col(4 * chunk);
 #pragma unroll
@@ -351,8 +387,8 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
       rq[j] = (uint32_t)(krow * 2 * T + (seg ^ turn) * 64 + col * 2);
     }
   }
-  auto read_p = [&](int st, int s, int i) { return *(const v8h*)(sP[st] + rp[s] + i * 32 * kRow); };
-  auto read_q = [&](int st, int s, int j) {
+  auto read_p = [&](int st, int s, int i) __attribute__((always_inline)) { return *(const v8h*)(sP[st] + rp[s] + i * 32 * kRow); };
+  auto read_q = [&](int st, int s, int j) __attribute__((always_inline)) {
     if constexpr (kSym) {
       return *(const v8h*)(sQ[st] + rq[s] + j * 32 * kRow);
     } else {
@@ -373,64 +409,66 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
+  // A step is four parts of 16 k, each with fragments of its own: part 0 reads those of parts 1 and 2, part 1 those of 3.
+  // Then every read of the stage is done, and a barrier frees it for the copies of the step after next.  A copy occupies
+  // the CU's address unit for 16 cycles, so that the waves' 16 F of them would stop the matrix cores if issued together:
+  // they are spread over parts 2 and 3 and the next step's part 0.  They have until the second barrier, before that step's
+  // part 3 reads the first fragments of what they bring.
+  constexpr int kAll = 2 * kCopies, kIn2 = (kAll + 2) / 3, kIn3 = (kAll + 1) / 3;
 #pragma unroll
-  for (int e = 0; e < kCopies; ++e) copy(0, e);
+  for (int n = 0; n < kAll; ++n) copy(0, n);
   advance();
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
   if (nk > 1) {
 #pragma unroll
-    for (int e = 0; e < kCopies; ++e) copy(1, e);
-    advance();
+    for (int n = 0; n < kIn2 + kIn3; ++n) copy(1, n);
   }
-  v8h fp[2][F], fq[2][F];
+  v8h fp[4][F], fq[4][F];
 #pragma unroll
   for (int i = 0; i < F; ++i) {
     fp[0][i] = read_p(0, 0, i);
     fq[0][i] = read_q(0, 0, i);
   }
   int st = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    const bool more = kt + 1 < nk, issue = kt + 2 < nk;
-    each<4>([&](auto part) {
-      constexpr int s = decltype(part)::value, now = s & 1, next = now ^ 1;
-      if constexpr (s == 3) {
-        // every read of this stage is done, and the next one has landed
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  auto one_step = [&](auto issue_, auto more_) __attribute__((always_inline)) {
+    constexpr bool issue = decltype(issue_)::value, more = decltype(more_)::value;
+    each<4>([&](auto part) __attribute__((always_inline)) {
+      constexpr int s = decltype(part)::value;
+      if constexpr (s == 2 && issue) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if constexpr (s == 3 && more) {
+        if constexpr (issue) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kIn2) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
       }
-      each<F * F>([&](auto index) {
+      each<F * F>([&](auto index) __attribute__((always_inline)) {
         constexpr int n = decltype(index)::value, i = n / F, j = n % F;
-        if constexpr (s < 3) {
-          if constexpr (n < F) {
-            fp[next][n] = read_p(st, s + 1, n);
-            fq[next][n] = read_q(st, s + 1, n);
+        // the fragments that go with this product: 2 F a part to read, 4 F in part 0
+        constexpr int reads = s == 0 ? 4 * F : s == 2 ? 0 : 2 * F, from = n * reads / (F * F), to = (n + 1) * reads / (F * F);
+        each<to - from>([&](auto k) __attribute__((always_inline)) {
+          constexpr int r = from + decltype(k)::value, set = s == 0 ? 1 + r / (2 * F) : s == 1 ? 3 : 0, f = r % (2 * F) / 2;
+          if constexpr (s < 2) {
+            if constexpr (r & 1) fq[set][f] = read_q(st, set, f);
+            else fp[set][f] = read_p(st, set, f);
+          } else if constexpr (more) {
+            if constexpr (r & 1) fq[0][f] = read_q(st ^ 1, 0, f);
+            else fp[0][f] = read_p(st ^ 1, 0, f);
           }
-        } else {
-          if constexpr (n < F) {
-            if (more) {
-              fp[next][n] = read_p(st ^ 1, 0, n);
-              fq[next][n] = read_q(st ^ 1, 0, n);
-            }
-          }
-        }
-        acc[i][j] = TRANS ? __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[now][i], fq[now][j], acc[i][j], 0, 0, 0)
-                          : __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[now][j], fp[now][i], acc[i][j], 0, 0, 0);
-        if constexpr (s == 3) {
-          constexpr int per = (kCopies + F * F - 1) / (F * F);
-          if (issue) {
-#pragma unroll
-            for (int e = n * per; e < (n + 1) * per; ++e)
-              if (e < kCopies) copy(st, e);
-          }
+        });
+        acc[i][j] = TRANS ? __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[s][i], fq[s][j], acc[i][j], 0, 0, 0)
+                          : __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[s][j], fp[s][i], acc[i][j], 0, 0, 0);
+        // and the copies: [first, first + here) of them in this part
+        constexpr bool active = s == 0 ? more : s >= 2 && issue;
+        constexpr int first = s == 2 ? 0 : s == 3 ? kIn2 : kIn2 + kIn3, here = s == 2 ? kIn2 : s == 3 ? kIn3 : kAll - first;
+        if constexpr (active) {
+          each<(n + 1) * here / (F * F) - n * here / (F * F)>([&](auto k) __attribute__((always_inline)) {
+            copy(s == 0 ? st ^ 1 : st, first + n * here / (F * F) + decltype(k)::value);
+          });
         }
         __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (s == 3) {
-        if (issue) advance();
-      }
+      if constexpr (s == 0 && more) advance();
     });
     st ^= 1;
-  }
-
+  };
   float keep = 1.0f, rate = 0.0f;
   if constexpr (MODE == kLast) {
     if (t.w != nullptr) {
@@ -439,56 +477,100 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
       rate = (float)(lr * t.scale);
     }
   }
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-#pragma unroll
-    for (int j = 0; j < F; ++j) {
-      // TRANS: the lane's column is l % 32 of strip j, its rows 16 h .. of strip i
-      const int m = m0 + wm + 32 * i + (TRANS ? 16 * h : l32), n = n0 + wn + 32 * j + (TRANS ? l32 : 16 * h);
-      if (m >= v.m || n >= (kSym ? v.m : v.n)) continue;
+  // The epilogue, a row of fragments at a time; what it reads is asked for two rows ahead, the first two before the last
+  // step's products.  TRANS: the lane's column is l % 32 of strip j, its rows 8 h .. and 16 + 8 h .. of strip i.  In the
+  // result's own rows a lane is always at row l % 32 and columns 8 h .. of a fragment: one offset a lane, and a uniform
+  // address for each fragment.
+  const int ld = MODE == kLast ? (t.w != nullptr ? t.cols : (int)t.ld_out) : kSym ? v.lm : v.ln;
+  const uint32_t own = (uint32_t)l32 * (uint32_t)ld + 8 * h;
+  // the first element of fragment (i, j) in rows of ld
+  auto first_of = [&](int i, int j) __attribute__((always_inline)) {
+    const int64_t m = m0 + wm + 32 * i, n = n0 + wn + 32 * j;
+    return TRANS ? n * ld + m : m * ld + n;
+  };
+  constexpr int kAhead = MODE == kGram ? 1 : MODE == kPoly ? 2 : 4;
+  u32x4 ahead[F < 3 ? F : 3][F][kAhead];
+  auto ask = [&](int i, u32x4 (&to)[F][kAhead]) __attribute__((always_inline)) {
+    each<F>([&](auto column) __attribute__((always_inline)) {
+      constexpr int j = decltype(column)::value;
+      if constexpr (MODE == kPoly) {
+        const half_t* base = uniform(v.a + first_of(i, j)) + own;
+        to[j][0] = *(const u32x4*)base;
+        to[j][1] = *(const u32x4*)(base + 16);
+      } else if constexpr (MODE == kStep) {
+        const half_t *hi = uniform(x + first_of(i, j)) + own, *lo = uniform(v.low + first_of(i, j)) + own;
+        to[j][0] = *(const u32x4*)hi;
+        to[j][1] = *(const u32x4*)lo;
+        to[j][2] = *(const u32x4*)(hi + 16);
+        to[j][3] = *(const u32x4*)(lo + 16);
+      } else if constexpr (MODE == kLast) {
+        const int row = (TRANS ? n0 + wn + 32 * j : m0 + wm + 32 * i) + l32;
+        const int col = (TRANS ? m0 + wm + 32 * i : n0 + wn + 32 * j) + 8 * h;
+        if (t.w == nullptr || row >= t.rows) return;
+        const float* base = uniform(t.w + first_of(i, j)) + own;
+        if (col + 8 <= t.cols) {
+          to[j][0] = ((const u32x4_any*)base)[0];
+          to[j][1] = ((const u32x4_any*)base)[1];
+        }
+        if (col + 24 <= t.cols) {
+          to[j][2] = ((const u32x4_any*)(base + 16))[0];
+          to[j][3] = ((const u32x4_any*)(base + 16))[1];
+        }
+      }
+    });
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  for (int kt = 2; kt < nk; ++kt) one_step(yes, yes);
+  if (nk > 1) one_step(no, yes);
+  ask(0, ahead[0]);
+  if constexpr (F > 1) ask(1, ahead[1]);
+  one_step(no, no);
+  each<F>([&](auto row) __attribute__((always_inline)) {
+    constexpr int i = decltype(row)::value;
+    if constexpr (i + 2 < F) ask(i + 2, ahead[(i + 2) % 3]);
+    __builtin_amdgcn_sched_barrier(0);
+    const auto& got = ahead[i % 3];
+    each<F>([&](auto column) __attribute__((always_inline)) {
+      constexpr int j = decltype(column)::value;
+      const int64_t first = first_of(i, j);
       const v16f d = acc[i][j];
-      if constexpr (MODE == kLast) {
-        float o[16];
+      each<2>([&](auto half) __attribute__((always_inline)) {
+        constexpr int q = decltype(half)::value;
+        if constexpr (MODE == kLast) {
+          float o[8];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[r] = d[r] * (1.0f / (kScaleX * kScaleF));
-        if constexpr (TRANS) finish(t, keep, rate, n, m, o);
-        else finish(t, keep, rate, m, n, o);
-      } else if constexpr (kSym) {
-        float o[16];
-        if constexpr (MODE == kGram) {
+          for (int r = 0; r < 8; ++r) o[r] = d[8 * q + r] * (1.0f / (kScaleX * kScaleF));
+          const u32x4 w[2] = {got[j][2 * q], got[j][2 * q + 1]};
+          const int row = (TRANS ? n0 + wn + 32 * j : m0 + wm + 32 * i) + l32;
+          const int col = (TRANS ? m0 + wm + 32 * i : n0 + wn + 32 * j) + 16 * q + 8 * h;
+          finish(t, keep, rate, row, col, first + 16 * q, own, o, w);
+        } else if constexpr (kSym) {
+          half_t* out = MODE == kGram ? v.a : v.b;
+          v8h y;
+          if constexpr (MODE == kGram) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = d[r] * (kScaleF / (kScaleX * kScaleX));
-        } else {
-          const v8h* base = (const v8h*)(v.a + (int64_t)m * v.m + n);
-          const v8h b0 = base[0], b1 = base[1];
+            for (int r = 0; r < 8; ++r) y[r] = (half_t)(d[8 * q + r] * (kScaleF / (kScaleX * kScaleX)));
+          } else {
+            const v8h base = __builtin_bit_cast(v8h, got[j][q]);
+            // the lane's row less its first column, where the diagonal may pass
+            const int off = m0 + wm + 32 * i + l32 - (n0 + wn + 32 * j + 16 * q + 8 * h);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            o[r] = fmaf(c.b, (float)(r < 8 ? b0[r & 7] : b1[r & 7]), d[r] * (c.c / kScaleF));
-            if (c.last && n + r == m) o[r] += c.a * kScaleF;
+            for (int r = 0; r < 8; ++r) {
+              float o = fmaf(c.b, (float)base[r], d[8 * q + r] * (c.c / kScaleF));
+              if (c.last && off == r) o += c.a * kScaleF;
+              y[r] = (half_t)o;
+            }
           }
-        }
-        half_t* out = MODE == kGram ? v.a : v.b;
-        v8h w0, w1;
+          *(v8h*)(uniform(out + first + 16 * q) + own) = y;
+          if (ti != tj) {
+            const uint32_t mirror = 8 * h * (uint32_t)ld + l32;
+            const int64_t at = (int64_t)(n0 + wn + 32 * j + 16 * q) * ld + m0 + wm + 32 * i;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          w0[r] = (half_t)o[r];
-          w1[r] = (half_t)o[8 + r];
-        }
-        v8h* to = (v8h*)(out + (int64_t)m * v.m + n);
-        to[0] = w0;
-        to[1] = w1;
-        if (ti != tj) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) out[(int64_t)(n + r) * v.m + m] = r < 8 ? w0[r & 7] : w1[r & 7];
-        }
-      } else {
-        const int64_t at = (int64_t)m * v.n + n;
-        const v8h* hi = (const v8h*)(x + at);
-        v8h* lo = (v8h*)(v.low + at);
-        v8h* to = (v8h*)((c.from ? v.x0 : v.x1) + at);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const v8h xh = hi[q], xl = lo[q];
+            for (int r = 0; r < 8; ++r) (uniform(out + at + (int64_t)r * ld))[mirror] = y[r];
+          }
+        } else {
+          const v8h xh = __builtin_bit_cast(v8h, got[j][2 * q]), xl = __builtin_bit_cast(v8h, got[j][2 * q + 1]);
           v8h nh, nl;
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
@@ -496,11 +578,20 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
             nh[r] = (half_t)y;
             nl[r] = (half_t)((y - (float)nh[r]) * kLow);
           }
-          to[q] = nh;
-          lo[q] = nl;
+          *(v8h*)(uniform((c.from ? v.x0 : v.x1) + first + 16 * q) + own) = nh;
+          *(v8h*)(uniform(v.low + first + 16 * q) + own) = nl;
         }
-      }
-    }
+      });
+      __builtin_amdgcn_sched_barrier(0);         // one fragment's registers at a time
+    });
+  });
+}
+
+// a's items by falling `key`, so that the longest tiles start first.
+template <typename Key>
+void sort_items(Args& a, const Key& key) {
+  for (int i = 1; i < a.count; ++i)
+    for (int k = i; k > 0 && key(a.item[k - 1]) < key(a.item[k]); --k) std::swap(a.item[k - 1], a.item[k]);
 }
 
 // Workgroups of each item, `of(item)` of them, as a's table; their number.
@@ -558,14 +649,18 @@ hipError_t launch_ortho(const OrthoItem* items, int count, const OrthoStep& step
     large += z.m * z.n;
   }
   const int f = large >= (int64_t)1 << 22 ? 4 : large >= (int64_t)1 << 18 ? 2 : 1;
+  // Gram: a tile's K is the longer side; the others: the shorter
+  Args by_n = a, by_m = a;
+  sort_items(by_n, [](const OrthoItem& t) { return t.rows > t.cols ? t.rows : t.cols; });
+  sort_items(by_m, [](const OrthoItem& t) { return t.rows < t.cols ? t.rows : t.cols; });
   Coef c{(float)step.a, (float)step.b, (float)step.c, 0, false};
   for (int k = 0; k < step.steps; ++k) {
     c.last = k + 1 == step.steps;
     c.from = k & 1;
-    products_of<kGram>(a, f, step, c, s);
-    products_of<kPoly>(a, f, step, c, s);
-    if (c.last) products_of<kLast>(a, f, step, c, s);
-    else products_of<kStep>(a, f, step, c, s);
+    products_of<kGram>(by_n, f, step, c, s);
+    products_of<kPoly>(by_m, f, step, c, s);
+    if (c.last) products_of<kLast>(by_m, f, step, c, s);
+    else products_of<kStep>(by_m, f, step, c, s);
   }
   return hipGetLastError();
 }

@@ -9,18 +9,21 @@
 namespace mx {
 
 constexpr int kOrthoGroup = 32;                    // matrices in one launch's arguments
-constexpr int kOrthoPad = 64;                      // sizes are padded to this: one K step of the products
+constexpr int kOrthoPad = 64;                      // one K step of the products: sizes are padded to it with zeros
+constexpr int kOrthoRest = 192;                    // room for the rest of the last tile of 256, which holds anything
 constexpr int64_t kOrthoSide = int64_t(1) << 20;   // rows and columns stay below
 constexpr int64_t kOrthoMinor = int64_t(1) << 16;  // the shorter side too
+constexpr int64_t kOrthoPitch = int64_t(1) << 26;  // elements between an output's rows stay below
 constexpr int kOrthoParts = 256;                   // sums of squares of a matrix at most
 constexpr int64_t kOrthoRun = 8192;                // elements for each of them at least
 
 inline int64_t ortho_pad(int64_t n) { return (n + kOrthoPad - 1) / kOrthoPad * kOrthoPad; }
 
 // A matrix's place in the workspace, in bytes: the sums of squares (float64), then X, the next X and X's low part
-// [m][n], A and B [m][m] in float16; m the shorter side, n the longer, both padded.
+// [m][n], A and B [m][m] in float16; m the shorter side, n the longer, each with room for a tile's rest.  (The rest also
+// keeps the rows of a matrix whose sides are powers of two out of step with the memory's channels.)
 struct OrthoSize {
-  int64_t m, n;                                    // padded
+  int64_t m, n;                                    // in whole K steps
   int64_t parts;                                   // sums of squares
   int64_t bytes;
 };
@@ -31,7 +34,8 @@ inline OrthoSize ortho_size(int64_t rows, int64_t cols) {
   s.n = ortho_pad(rows < cols ? cols : rows);
   s.parts = (rows * cols + kOrthoRun - 1) / kOrthoRun;
   if (s.parts > kOrthoParts) s.parts = kOrthoParts;
-  s.bytes = 8 * kOrthoParts + 2 * (3 * s.m * s.n + 2 * s.m * s.m);
+  const int64_t lm = s.m + kOrthoRest, ln = s.n + kOrthoRest;
+  s.bytes = 8 * kOrthoParts + 2 * (3 * lm * ln + 2 * lm * lm);
   return s;
 }
 

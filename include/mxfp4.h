@@ -581,8 +581,8 @@ typedef struct {
  *              count; entries with rows or cols 0 are skipped; rows and cols <
  *              2^20, the smaller of them < 2^16
  *   g, out     device, row-major, aligned to their element, ld_g and ld_out
- *              elements between rows, >= cols; no out may overlap another, a g
- *              of any entry or the workspace
+ *              elements between rows, >= cols, ld_out < 2^26; no out may overlap
+ *              another, a g of any entry or the workspace
  *   workspace  16-byte aligned device memory of at least
  *              mx_orthogonalize_workspace bytes, this call's alone until it has
  *              run; it needs no initial value

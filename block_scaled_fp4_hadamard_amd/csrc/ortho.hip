@@ -11,12 +11,13 @@
 // Number formats.  The products are float16 with float32 sums: 11 bits at the
 // rate of bf16's 8, and the range suffices because everything is bounded (no
 // entry of X above |X|_2, about 1.2 for the usual coefficients).  X is held
-// times 2^12, A and B times 2^11, so that the small entries of large matrices
-// (1 / sqrt(m n) in X, 1 / m in A) stay normal numbers.  Rounding X costs most:
+// times 2^12 and A times 2^11, so that the small entries of large matrices
+// (1 / sqrt(m n) in X, 1 / m in A) stay normal numbers; B adds to a I, beside
+// which its subnormal entries, off by 2^-25, are nothing.  Rounding X costs most:
 // what it adds in weak directions grows by a in every step, to a share of the
 // result where U has few strong directions.  So X is held in two parts, high and
-// low (times 2^11), 22 bits together; the products read the high part, and the
-// sum a X takes both.  Against float64 the result is off by 0.9e-3 to 1.6e-3 of
+// low, 22 bits together (to 2^-25 in the low part's own scale); the products read
+// the high part, and the sum a X takes both.  Against float64 the result is off by 0.9e-3 to 1.6e-3 of
 // its norm, below what rounding it to bf16 costs (1.7e-3); with the high part
 // alone a matrix of rank 1 was 15% off.
 #include <hip/hip_runtime.h>
@@ -37,9 +38,8 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kXcds = 8;
 constexpr int kRow = 128;                // bytes of an operand's row in one K step: 64 values
-constexpr float kScaleX = 0x1p12f, kScaleF = 0x1p11f, kLow = 0x1p11f;
+constexpr float kScaleX = 0x1p12f, kScaleA = 0x1p11f;
 
 struct Args {
   OrthoItem item[kOrthoGroup];
@@ -85,6 +85,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
+// 16 bytes wherever a row may start: one access, whatever the row pitch and the width
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (T*)(((uint64_t)hi << 32) | lo);
+}
+// a pointer known to be the same in all lanes and to lie in global memory (not in LDS or scratch)
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(1))) T* global(T* p) {
+  return (__attribute__((address_space(1))) T*)uniform(p);
+}
+template <typename V, typename P>
+__device__ __forceinline__ V load_at(P p) {
+  return *(const __attribute__((address_space(1))) V*)p;
+}
+template <typename V, typename P>
+__device__ __forceinline__ void store_at(P p, const V& x) {
+  *(__attribute__((address_space(1))) V*)p = x;
+}
+template <typename P>
+__device__ __forceinline__ void store8(P p, const float (&y)[8]) {
+  store_at<u32x4_any>(p, u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])});
+  store_at<u32x4_any>(p + 4, u32x4{__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])});
+}
+
 // ---------------------------------------------------------------------------
 // The moment and the sum of squares: m = RN(RN(m mu) + RN(g (1 - mu))), and u =
 // RN(RN(g (1 - mu)) + RN(m mu)) (Nesterov) or m.  Squares are added in float64,
@@ -99,12 +128,43 @@ __device__ __forceinline__ float update_of(float g, float m, const Moment& c) {
   return c.nesterov ? g * c.rest + m * c.mu : m;
 }
 
-__device__ __forceinline__ float gradient(const OrthoItem& t, int64_t at) {
-  return t.g_bf16 ? bf16_value(((const uint16_t*)t.g)[at]) : ((const float*)t.g)[at];
-}
-
 __device__ __forceinline__ Moment moment_of(const OrthoStep& s) {
   return Moment{s.momentum, s.rest, s.grad_scale ? *s.grad_scale : 1.0f, s.nesterov};
+}
+
+// `count` <= N values of a gradient or moment from p on, as float32; zeros after them
+template <int N>
+__device__ __forceinline__ void load_values(const float* p, int count, float (&o)[N]) {
+#pragma unroll
+  for (int q = 0; q < N; q += 4) {
+    if (q + 4 <= count) {
+      const u32x4 r = *(const u32x4_any*)(p + q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[q + e] = __uint_as_float(r[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[q + e] = q + e < count ? p[q + e] : 0.0f;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_values(const uint16_t* p, int count, float (&o)[N]) {
+  if (count >= N) {
+    uint32_t r[N / 2];
+    __builtin_memcpy(r, p, sizeof(r));
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = __uint_as_float((e & 1) ? r[e >> 1] & 0xFFFF0000u : r[e >> 1] << 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = e < count ? bf16_value(p[e]) : 0.0f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_gradient(const OrthoItem& t, int64_t at, int count, float scale, float (&o)[N]) {
+  if (t.g_bf16) load_values((const uint16_t*)t.g + at, count, o);
+  else load_values((const float*)t.g + at, count, o);
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] *= scale;
 }
 
 constexpr int kSumThreads = 1024;
@@ -117,18 +177,36 @@ __global__ void __launch_bounds__(kSumThreads) ortho_sum(const Args a, const Ort
   const View v = view(t);
   const Moment c = moment_of(step);
   const int64_t total = (int64_t)t.rows * t.cols, parts = min((int64_t)kOrthoParts, (total + kOrthoRun - 1) / kOrthoRun);
-  const int64_t each = (total + parts - 1) / parts, from = id * each, to = min(total, from + each);
+  // a contiguous gradient is one long row, of which a part is a run; otherwise a part is a run of rows
+  const bool one = t.ld_g == t.cols;
+  const int64_t rows = one ? 1 : t.rows, cols = one ? total : t.cols, units = one ? (total + 7) / 8 : t.rows;
+  const int64_t each = (units + parts - 1) / parts, from = min(units, id * each), to = min(units, from + each);
+  const int64_t row0 = one ? 0 : from, row1 = one ? 1 : to, col0 = one ? 8 * from : 0, col1 = one ? min(cols, 8 * to) : cols;
   double sum = 0.0;
-  for (int64_t at = from + threadIdx.x; at < to; at += kSumThreads) {
-    const int64_t row = at / t.cols, col = at - row * t.cols;
-    float u = gradient(t, row * t.ld_g + col) * c.scale;
-    if (t.moment != nullptr) {
-      const float m = t.moment[at] * c.mu + u * c.rest;
-      t.moment[at] = m;
-      u = update_of(u, m, c);
+  for (int64_t row = row0; row < row1; ++row)
+    for (int64_t col = col0 + 8 * threadIdx.x; col < col1; col += 8 * kSumThreads) {
+      const int count = (int)min((int64_t)8, col1 - col);
+      float u[8];
+      load_gradient(t, row * t.ld_g + col, count, c.scale, u);
+      if (t.moment != nullptr) {               // moments and their gradients are contiguous
+        float m[8];
+        load_values(t.moment + col, count, m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          m[e] = m[e] * c.mu + u[e] * c.rest;
+          u[e] = update_of(u[e], m[e], c);
+        }
+        if (count == 8) {
+          store8(t.moment + col, m);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < count) t.moment[col + e] = m[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += (double)u[e] * (double)u[e];
     }
-    sum += (double)u * (double)u;
-  }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
@@ -151,34 +229,66 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
   const Moment c = moment_of(step);
   const int64_t total = (int64_t)t.rows * t.cols;
   const int parts = (int)min((int64_t)kOrthoParts, (total + kOrthoRun - 1) / kOrthoRun);
-  double sum = (int)threadIdx.x < parts ? v.parts[threadIdx.x] : 0.0;
+  const double mine = (int)threadIdx.x < parts ? v.parts[threadIdx.x] : 0.0;
+  const bool tall = t.rows > t.cols;
+  const int across = v.n / 64, m0 = id / across * 64, n0 = id % across * 64;
+  const int r0 = tall ? n0 : m0, c0 = tall ? m0 : n0;          // the piece in U
+  // a lane takes four neighbouring values of every 16th row, asked for before the sums are added
+  const int row = threadIdx.x / 16, col = 4 * (threadIdx.x % 16);
+  float u[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + row + 16 * i, count = r < t.rows ? min(4, t.cols - (c0 + col)) : 0;
+    if (count <= 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[i][e] = 0.0f;
+      continue;
+    }
+    load_gradient(t, (int64_t)r * t.ld_g + c0 + col, count, c.scale, u[i]);
+    if (t.moment != nullptr) {
+      float m[4];
+      load_values(t.moment + (int64_t)r * t.cols + c0 + col, count, m);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[i][e] = update_of(u[i][e], m[e], c);
+    }
+  }
+  double sum = mine;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
   sum = (red[0] + red[1]) + (red[2] + red[3]);
   const double scale = (double)kScaleX / (sqrt(sum) + step.eps);
-  const bool tall = t.rows > t.cols;
-  const int across = v.n / 64, m0 = id / across * 64, n0 = id % across * 64;
-  const int r0 = tall ? n0 : m0, c0 = tall ? m0 : n0;          // the piece in U
-  for (int i = threadIdx.x; i < 4096; i += 256) {
-    const int r = r0 + i / 64, k = c0 + i % 64;
-    float x = 0.0f;
-    if (r < t.rows && k < t.cols) {
-      const float g = gradient(t, (int64_t)r * t.ld_g + k) * c.scale;
-      const float u = t.moment != nullptr ? update_of(g, t.moment[(int64_t)r * t.cols + k], c) : g;
-      x = (float)((double)u * scale);
+  auto put = [&](int m, int n, const float (&x)[4]) {
+    v4h hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi[e] = (half_t)x[e];
+      lo[e] = (half_t)(x[e] - (float)hi[e]);
     }
-    if (tall) piece[i % 64][i / 64] = x;
-    else piece[i / 64][i % 64] = x;
+    const int64_t at = (int64_t)(m0 + m) * v.ln + n0 + n;
+    *(v4h*)(v.x0 + at) = hi;
+    *(v4h*)(v.low + at) = lo;
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[i][e] = (float)((double)u[i][e] * scale);
+    if (!tall) {
+      put(row + 16 * i, col, u[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) piece[col + e][row + 16 * i] = u[i][e];
+    }
   }
+  if (!tall) return;
   __syncthreads();
-  for (int i = threadIdx.x; i < 4096; i += 256) {
-    const float x = piece[i / 64][i % 64];
-    const half_t hi = (half_t)x;
-    const int64_t at = (int64_t)(m0 + i / 64) * v.ln + n0 + i % 64;
-    v.x0[at] = hi;
-    v.low[at] = (half_t)((x - (float)hi) * kLow);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = piece[row + 16 * i][col + e];
+    put(row + 16 * i, col, x);
   }
 }
 
@@ -186,7 +296,7 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 // The products: a workgroup of four waves takes a tile of the result, 64 F by 64
 // F, each wave a quarter of it, F x F fragments of the 32x32x16 instruction.
 // K advances 64 values (128 bytes of every row) a step, copied global -> LDS by
-// DMA into one of two stages while the other is consumed.
+// DMA into one of a ring of stages while another is consumed.
 //
 //   kGram  A = X X^T            both operands K-contiguous
 //   kPoly  B = b A + c A A      the same, A being its own transpose
@@ -222,12 +332,14 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
-template <typename T>
-__device__ __forceinline__ T* uniform(T* p) {
-  const uint64_t v = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (T*)(((uint64_t)hi << 32) | lo);
+// Transposing LDS reads: in each 16 lanes, lane s gives the address of four neighbouring values of row s / 4, and gets
+// the four rows' values of column s.
+__device__ __forceinline__ v8h read_columns(const uint8_t* rows03, const uint8_t* rows47) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  const v4h lo = __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)rows03));
+  const v4h hi = __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)rows47));
+  return v8h{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 template <int... I, typename F>
 __device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& f) {
@@ -238,9 +350,6 @@ __device__ __forceinline__ void each(const F& f) {
   each(std::make_integer_sequence<int, N>{}, f);
 }
 
-// 16 bytes wherever a row may start: one access, whatever the row pitch and the width
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
 // What the last step writes: eight neighbouring results in row `row` of U's layout, from column `col`, the lane's `own`
 // elements on from the wave's element `first`.  `w`: the weights there, read ahead where all eight exist.
 __device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rate, int row, int col, int64_t first,
@@ -250,8 +359,8 @@ __device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rat
   const int left = t.cols - col;
   float y[8];
   if (t.w != nullptr) {
-    float* to = uniform(t.w + first) + own;
-    uint16_t* copy = uniform(t.copy + first) + own;
+    const auto to = global(t.w + first) + own;
+    const auto copy = global(t.copy + first) + own;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float old = left >= 8 ? __uint_as_float(w[e >> 2][e & 3]) : e < left ? to[e] : 0.0f;
@@ -259,9 +368,8 @@ __device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rat
     }
     const u32x4 h = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
     if (left >= 8) {
-      ((u32x4_any*)to)[0] = u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
-      ((u32x4_any*)to)[1] = u32x4{__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])};
-      if (t.copy != nullptr) *(u32x4_any*)copy = h;
+      store8(to, y);
+      if (t.copy != nullptr) store_at<u32x4_any>(copy, h);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -272,16 +380,14 @@ __device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rat
     }
     return;
   }
-  uint16_t* out16 = uniform((uint16_t*)t.out + first) + own;
-  float* out32 = uniform((float*)t.out + first) + own;
+  const auto out16 = global((uint16_t*)t.out + first) + own;
+  const auto out32 = global((float*)t.out + first) + own;
   const u32x4 h = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])};
   if (left >= 8) {
     if (t.out_bf16) {
-      *(u32x4_any*)out16 = h;
+      store_at<u32x4_any>(out16, h);
     } else {
-      u32x4_any* to = (u32x4_any*)out32;
-      to[0] = u32x4{__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])};
-      to[1] = u32x4{__float_as_uint(o[4]), __float_as_uint(o[5]), __float_as_uint(o[6]), __float_as_uint(o[7])};
+      store8(out32, o);
     }
   } else {
 #pragma unroll
@@ -299,11 +405,12 @@ struct Coef {
   bool last;
 };
 
-template <int F, int MODE, bool TRANS>
-__global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args a, const OrthoStep step, const Coef c) {
+template <int F, int S, int MODE, bool TRANS>
+__global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a, const OrthoStep step, const Coef c) {
   constexpr bool kSym = MODE == kGram || MODE == kPoly;
   constexpr int T = 64 * F, kStage = T * kRow;
-  __shared__ __attribute__((aligned(1024))) uint8_t sP[2][kStage], sQ[2][kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S * kStage];      // the first operand's stages, the second's
+  uint8_t *const sP = lds, *const sQ = lds + S * kStage;
   int id;
   const OrthoItem t = a.item[find(a, id)];
   if (!kSym && MODE == kLast && (t.rows > t.cols) != TRANS) return;
@@ -339,6 +446,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
   // copies a quarter of each operand.  Rows and columns past the matrix hold anything: each spoils its own row or column of
   // the result, which lies past the matrix too.
   constexpr int kCopies = 2 * F;
+  constexpr bool kOdd = F % 2 != 0;        // K rows of an odd number of 128 bytes already part the banks of neighbours
   uint32_t op[kCopies], oq[kCopies];
 #pragma unroll
   for (int e = 0; e < kCopies; ++e) {
@@ -351,7 +459,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
     } else {
       // K row k of T values, its 64-byte pieces in an order that parts four neighbouring rows' banks
       const int at = (wave * kCopies + e) * 1024 + lane * 16, k = at / (2 * T), piece = at % (2 * T) / 16;
-      const int turn = F == 1 ? (k >> 1) & 1 : k & 3;
+      const int turn = kOdd ? (k >> 1) & 1 : k & 3;
       const int col = 8 * ((((piece >> 2) ^ turn) << 2) + (piece & 3));
       oq[e] = (uint32_t)k * (uint32_t)(2 * ldq) + (uint32_t)(2 * col);
     }
@@ -359,7 +467,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
   const uint8_t* cp = uniform((const uint8_t*)(pp + (int64_t)m0 * ldp));
   const uint8_t* cq = uniform((const uint8_t*)(kSym ? qq + (int64_t)n0 * ldq : qq + n0));
   const int64_t stepq = kSym ? kRow : (int64_t)128 * ldq;          // 64 values, or 64 rows
-  const uint32_t dP = lds_addr(&sP[0][wave * kCopies * 1024]), dQ = lds_addr(&sQ[0][wave * kCopies * 1024]);
+  const uint32_t dP = lds_addr(sP + wave * kCopies * 1024), dQ = lds_addr(sQ + wave * kCopies * 1024);
   auto copy = [&](int st, int n) __attribute__((always_inline)) {
     if (n & 1) dma16(cq, oq[n >> 1], dQ + st * kStage + (n >> 1) * 1024);
     else dma16(cp, op[n >> 1], dP + st * kStage + (n >> 1) * 1024);
@@ -383,21 +491,17 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
     const int col = TRANS ? 4 * chunk : strip_col(4 * chunk);
 #pragma unroll
     for (int j = 0; j < F; ++j) {
-      const int seg = (wn >> 5) + j, turn = F == 1 ? (krow >> 1) & 1 : krow & 3;
+      const int seg = (wn >> 5) + j, turn = kOdd ? (krow >> 1) & 1 : krow & 3;
       rq[j] = (uint32_t)(krow * 2 * T + (seg ^ turn) * 64 + col * 2);
     }
   }
-  auto read_p = [&](int st, int s, int i) __attribute__((always_inline)) { return *(const v8h*)(sP[st] + rp[s] + i * 32 * kRow); };
+  auto read_p = [&](int st, int s, int i) __attribute__((always_inline)) { return *(const v8h*)(sP + st * kStage + rp[s] + i * 32 * kRow); };
   auto read_q = [&](int st, int s, int j) __attribute__((always_inline)) {
     if constexpr (kSym) {
-      return *(const v8h*)(sQ[st] + rq[s] + j * 32 * kRow);
+      return *(const v8h*)(sQ + st * kStage + rq[s] + j * 32 * kRow);
     } else {
-      typedef short v4s __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) v4s lds_v4s;
-      const uint8_t* p = sQ[st] + rq[j] + s * 16 * 2 * T;
-      const v4h lo = __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p));
-      const v4h hi = __builtin_bit_cast(v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * T)));
-      return v8h{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      const uint8_t* p = sQ + st * kStage + rq[j] + s * 16 * 2 * T;
+      return read_columns(p, p + 4 * 2 * T);
     }
   };
 
@@ -410,33 +514,36 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   // A step is four parts of 16 k, each with fragments of its own: part 0 reads those of parts 1 and 2, part 1 those of 3.
-  // Then every read of the stage is done, and a barrier frees it for the copies of the step after next.  A copy occupies
+  // Then every read of the stage is done, and a barrier frees it for the copies of the step S further on.  A copy occupies
   // the CU's address unit for 16 cycles, so that the waves' 16 F of them would stop the matrix cores if issued together:
-  // they are spread over parts 2 and 3 and the next step's part 0.  They have until the second barrier, before that step's
-  // part 3 reads the first fragments of what they bring.
+  // they are spread over parts 2 and 3 and the next step's part 0.  A second barrier, before part 3 reads the next step's
+  // first fragments, waits for the copies that bring them.
   constexpr int kAll = 2 * kCopies, kIn2 = (kAll + 2) / 3, kIn3 = (kAll + 1) / 3;
 #pragma unroll
-  for (int n = 0; n < kAll; ++n) copy(0, n);
-  advance();
-  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  if (nk > 1) {
+  for (int b = 0; b < S; ++b) {
+    if (b >= nk) break;
+    // the last stage's batch is left to step 0 in part, as every later batch to the step after
 #pragma unroll
-    for (int n = 0; n < kIn2 + kIn3; ++n) copy(1, n);
+    for (int n = 0; n < (b + 1 < S ? kAll : kIn2 + kIn3); ++n) copy(b, n);
+    if (b + 1 < S) advance();
   }
+  if (nk >= S) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 2) * kAll + kIn2 + kIn3) : "memory");
+  else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
   v8h fp[4][F], fq[4][F];
 #pragma unroll
   for (int i = 0; i < F; ++i) {
     fp[0][i] = read_p(0, 0, i);
     fq[0][i] = read_q(0, 0, i);
   }
-  int st = 0;
-  auto one_step = [&](auto issue_, auto more_) __attribute__((always_inline)) {
-    constexpr bool issue = decltype(issue_)::value, more = decltype(more_)::value;
+  int st = 0, last = S - 1;              // the step's stage, and the one before it
+  auto one_step = [&](auto finish_, auto issue_, auto more_) __attribute__((always_inline)) {
+    constexpr bool ends = decltype(finish_)::value, issue = decltype(issue_)::value, more = decltype(more_)::value;
+    const int next = st + 1 == S ? 0 : st + 1;
     each<4>([&](auto part) __attribute__((always_inline)) {
       constexpr int s = decltype(part)::value;
       if constexpr (s == 2 && issue) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if constexpr (s == 3 && more) {
-        if constexpr (issue) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kIn2) : "memory");
+        if constexpr (issue) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 2) * kAll + kIn2) : "memory");
         else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
       }
       each<F * F>([&](auto index) __attribute__((always_inline)) {
@@ -449,25 +556,26 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
             if constexpr (r & 1) fq[set][f] = read_q(st, set, f);
             else fp[set][f] = read_p(st, set, f);
           } else if constexpr (more) {
-            if constexpr (r & 1) fq[0][f] = read_q(st ^ 1, 0, f);
-            else fp[0][f] = read_p(st ^ 1, 0, f);
+            if constexpr (r & 1) fq[0][f] = read_q(next, 0, f);
+            else fp[0][f] = read_p(next, 0, f);
           }
         });
         acc[i][j] = TRANS ? __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[s][i], fq[s][j], acc[i][j], 0, 0, 0)
                           : __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[s][j], fp[s][i], acc[i][j], 0, 0, 0);
         // and the copies: [first, first + here) of them in this part
-        constexpr bool active = s == 0 ? more : s >= 2 && issue;
+        constexpr bool active = s == 0 ? ends : s >= 2 && issue;
         constexpr int first = s == 2 ? 0 : s == 3 ? kIn2 : kIn2 + kIn3, here = s == 2 ? kIn2 : s == 3 ? kIn3 : kAll - first;
         if constexpr (active) {
           each<(n + 1) * here / (F * F) - n * here / (F * F)>([&](auto k) __attribute__((always_inline)) {
-            copy(s == 0 ? st ^ 1 : st, first + n * here / (F * F) + decltype(k)::value);
+            copy(s == 0 ? last : st, first + n * here / (F * F) + decltype(k)::value);
           });
         }
         __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (s == 0 && more) advance();
+      if constexpr (s == 0 && ends) advance();
     });
-    st ^= 1;
+    last = st;
+    st = next;
   };
   float keep = 1.0f, rate = 0.0f;
   if constexpr (MODE == kLast) {
@@ -494,38 +602,53 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
     each<F>([&](auto column) __attribute__((always_inline)) {
       constexpr int j = decltype(column)::value;
       if constexpr (MODE == kPoly) {
-        const half_t* base = uniform(v.a + first_of(i, j)) + own;
-        to[j][0] = *(const u32x4*)base;
-        to[j][1] = *(const u32x4*)(base + 16);
+        const auto base = global(v.a + first_of(i, j)) + own;
+        to[j][0] = load_at<u32x4>(base);
+        to[j][1] = load_at<u32x4>(base + 16);
       } else if constexpr (MODE == kStep) {
-        const half_t *hi = uniform(x + first_of(i, j)) + own, *lo = uniform(v.low + first_of(i, j)) + own;
-        to[j][0] = *(const u32x4*)hi;
-        to[j][1] = *(const u32x4*)lo;
-        to[j][2] = *(const u32x4*)(hi + 16);
-        to[j][3] = *(const u32x4*)(lo + 16);
+        const auto hi = global(x + first_of(i, j)) + own;
+        const auto lo = global(v.low + first_of(i, j)) + own;
+        to[j][0] = load_at<u32x4>(hi);
+        to[j][1] = load_at<u32x4>(lo);
+        to[j][2] = load_at<u32x4>(hi + 16);
+        to[j][3] = load_at<u32x4>(lo + 16);
       } else if constexpr (MODE == kLast) {
         const int row = (TRANS ? n0 + wn + 32 * j : m0 + wm + 32 * i) + l32;
         const int col = (TRANS ? m0 + wm + 32 * i : n0 + wn + 32 * j) + 8 * h;
         if (t.w == nullptr || row >= t.rows) return;
-        const float* base = uniform(t.w + first_of(i, j)) + own;
+        const auto base = global(t.w + first_of(i, j)) + own;
         if (col + 8 <= t.cols) {
-          to[j][0] = ((const u32x4_any*)base)[0];
-          to[j][1] = ((const u32x4_any*)base)[1];
+          to[j][0] = load_at<u32x4_any>(base);
+          to[j][1] = load_at<u32x4_any>(base + 4);
         }
         if (col + 24 <= t.cols) {
-          to[j][2] = ((const u32x4_any*)(base + 16))[0];
-          to[j][3] = ((const u32x4_any*)(base + 16))[1];
+          to[j][2] = load_at<u32x4_any>(base + 16);
+          to[j][3] = load_at<u32x4_any>(base + 20);
         }
       }
     });
   };
   constexpr std::true_type yes;
   constexpr std::false_type no;
-  for (int kt = 2; kt < nk; ++kt) one_step(yes, yes);
-  if (nk > 1) one_step(no, yes);
+  int kt = 0;
+  for (; kt + S < nk; ++kt) one_step(yes, yes, yes);
+  if (nk >= S) {
+    one_step(yes, no, yes);
+    ++kt;
+  }
+  for (; kt + 1 < nk; ++kt) one_step(no, no, yes);
   ask(0, ahead[0]);
   if constexpr (F > 1) ask(1, ahead[1]);
-  one_step(no, no);
+  one_step(no, no, no);
+  // The other half of a symmetric result goes through LDS, a wave's part [row][column] in its own quarter, and leaves by
+  // transposing reads as rows of 16 bytes.
+  uint8_t* const turn = lds + wave * (32 * F * 64 * F);
+  auto side = [&](int row, int col) __attribute__((always_inline)) {
+    // 32-byte pieces in an order that parts the banks of the eight rows of a read
+    const int unit = (col >> 4) ^ (F == 4 ? (row & 3) | ((row >> 1) & 4) : 0);
+    return row * 64 * F + unit * 32 + 2 * (col & 15);
+  };
+  if constexpr (kSym) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   each<F>([&](auto row) __attribute__((always_inline)) {
     constexpr int i = decltype(row)::value;
     if constexpr (i + 2 < F) ask(i + 2, ahead[(i + 2) % 3]);
@@ -540,7 +663,7 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
         if constexpr (MODE == kLast) {
           float o[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) o[r] = d[8 * q + r] * (1.0f / (kScaleX * kScaleF));
+          for (int r = 0; r < 8; ++r) o[r] = d[8 * q + r] * (1.0f / kScaleX);
           const u32x4 w[2] = {got[j][2 * q], got[j][2 * q + 1]};
           const int row = (TRANS ? n0 + wn + 32 * j : m0 + wm + 32 * i) + l32;
           const int col = (TRANS ? m0 + wm + 32 * i : n0 + wn + 32 * j) + 16 * q + 8 * h;
@@ -550,41 +673,50 @@ __global__ void __launch_bounds__(256, F == 4 ? 1 : 2) ortho_product(const Args 
           v8h y;
           if constexpr (MODE == kGram) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) y[r] = (half_t)(d[8 * q + r] * (kScaleF / (kScaleX * kScaleX)));
+            for (int r = 0; r < 8; ++r) y[r] = (half_t)(d[8 * q + r] * (kScaleA / (kScaleX * kScaleX)));
           } else {
             const v8h base = __builtin_bit_cast(v8h, got[j][q]);
             // the lane's row less its first column, where the diagonal may pass
             const int off = m0 + wm + 32 * i + l32 - (n0 + wn + 32 * j + 16 * q + 8 * h);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-              float o = fmaf(c.b, (float)base[r], d[8 * q + r] * (c.c / kScaleF));
-              if (c.last && off == r) o += c.a * kScaleF;
+              float o = fmaf(c.b / kScaleA, (float)base[r], d[8 * q + r] * (c.c / (kScaleA * kScaleA)));
+              if (c.last && off == r) o += c.a;
               y[r] = (half_t)o;
             }
           }
-          *(v8h*)(uniform(out + first + 16 * q) + own) = y;
-          if (ti != tj) {
-            const uint32_t mirror = 8 * h * (uint32_t)ld + l32;
-            const int64_t at = (int64_t)(n0 + wn + 32 * j + 16 * q) * ld + m0 + wm + 32 * i;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) (uniform(out + at + (int64_t)r * ld))[mirror] = y[r];
-          }
+          store_at(global(out + first + 16 * q) + own, y);
+          if (ti != tj) *(v8h*)(turn + side(32 * i + l32, 32 * j + 16 * q + 8 * h)) = y;
         } else {
           const v8h xh = __builtin_bit_cast(v8h, got[j][2 * q]), xl = __builtin_bit_cast(v8h, got[j][2 * q + 1]);
           v8h nh, nl;
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const float y = fmaf(c.a, fmaf((float)xl[r], 1.0f / kLow, (float)xh[r]), d[8 * q + r] * (1.0f / kScaleF));
+            const float y = fmaf(c.a, (float)xl[r] + (float)xh[r], d[8 * q + r]);
             nh[r] = (half_t)y;
-            nl[r] = (half_t)((y - (float)nh[r]) * kLow);
+            nl[r] = (half_t)(y - (float)nh[r]);
           }
-          *(v8h*)(uniform((c.from ? v.x0 : v.x1) + first + 16 * q) + own) = nh;
-          *(v8h*)(uniform(v.low + first + 16 * q) + own) = nl;
+          store_at(global((c.from ? v.x0 : v.x1) + first + 16 * q) + own, nh);
+          store_at(global(v.low + first + 16 * q) + own, nl);
         }
       });
       __builtin_amdgcn_sched_barrier(0);         // one fragment's registers at a time
     });
   });
+  if constexpr (kSym) {
+    if (ti == tj) return;
+    half_t* out = MODE == kGram ? v.a : v.b;
+    const int s = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < 32 * F; n += 16)
+#pragma unroll
+      for (int m = 0; m < 32 * F; m += 32) {
+        // 16 columns of 32 rows: a lane takes column n + s and rows m + 8 g ..
+        const int row = m + 8 * g + (s >> 2), col = n + 4 * (s & 3);
+        const v8h y = read_columns(turn + side(row, col), turn + side(row + 4, col));
+        store_at(global(out + (int64_t)(n0 + wn + n) * ld + m0 + wm + m) + ((uint32_t)s * (uint32_t)ld + 8 * g), y);
+      }
+  }
 }
 
 // a's items by falling `key`, so that the longest tiles start first.
@@ -605,29 +737,38 @@ int deal(Args& a, const Of& of) {
   return total;
 }
 
-template <int F, int MODE>
+template <int F, int S, int MODE>
 void products(Args& a, const OrthoStep& step, const Coef& c, hipStream_t s) {
-  constexpr int T = 64 * F;
   const int total = deal(a, [&](const OrthoItem& t) {
     const OrthoSize z = ortho_size(t.rows, t.cols);
-    const int64_t tm = (z.m + T - 1) / T, tn = (z.n + T - 1) / T;
-    const int64_t tiles = MODE == kGram || MODE == kPoly ? tm * (tm + 1) / 2 : tm * tn;
-    return (int)((tiles + kXcds - 1) / kXcds * kXcds);
+    return (int)((ortho_tiles(z, MODE == kGram || MODE == kPoly, F) + kXcds - 1) / kXcds * kXcds);
   });
   bool wide = MODE != kLast, tall = false;
   if (MODE == kLast)
     for (int i = 0; i < a.count; ++i) (a.item[i].rows > a.item[i].cols ? tall : wide) = true;
-  if (wide) hipLaunchKernelGGL((ortho_product<F, MODE, false>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
+  if (wide) hipLaunchKernelGGL((ortho_product<F, S, MODE, false>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
   if constexpr (MODE == kLast) {
-    if (tall) hipLaunchKernelGGL((ortho_product<F, MODE, true>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
+    if (tall) hipLaunchKernelGGL((ortho_product<F, S, MODE, true>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
   }
 }
 
+// The tile whose time for these items is the least.
 template <int MODE>
-void products_of(Args& a, int f, const OrthoStep& step, const Coef& c, hipStream_t s) {
-  if (f == 4) products<4, MODE>(a, step, c, s);
-  else if (f == 2) products<2, MODE>(a, step, c, s);
-  else products<1, MODE>(a, step, c, s);
+OrthoTile tile_of(const Args& a) {
+  OrthoSize sizes[kOrthoGroup];
+  for (int i = 0; i < a.count; ++i) sizes[i] = ortho_size(a.item[i].rows, a.item[i].cols);
+  return ortho_choose(sizes, a.count, MODE == kGram || MODE == kPoly, MODE == kGram);
+}
+
+template <int MODE>
+void products_of(Args& a, OrthoTile tile, const OrthoStep& step, const Coef& c, hipStream_t s) {
+  switch (tile) {
+    case OrthoTile::k64: products<1, 4, MODE>(a, step, c, s); break;
+    case OrthoTile::k128: products<2, 3, MODE>(a, step, c, s); break;
+    case OrthoTile::k128Two: products<2, 2, MODE>(a, step, c, s); break;
+    case OrthoTile::k192: products<3, 3, MODE>(a, step, c, s); break;
+    case OrthoTile::k256: products<4, 2, MODE>(a, step, c, s); break;
+  }
 }
 
 }  // namespace
@@ -643,24 +784,19 @@ hipError_t launch_ortho(const OrthoItem* items, int count, const OrthoStep& step
     return (int)(z.m / 64 * (z.n / 64));
   });
   hipLaunchKernelGGL(ortho_start, dim3((unsigned)total), dim3(256), 0, s, a, step);
-  int64_t large = 0;
-  for (int i = 0; i < count; ++i) {
-    const OrthoSize z = ortho_size(a.item[i].rows, a.item[i].cols);
-    large += z.m * z.n;
-  }
-  const int f = large >= (int64_t)1 << 22 ? 4 : large >= (int64_t)1 << 18 ? 2 : 1;
   // Gram: a tile's K is the longer side; the others: the shorter
   Args by_n = a, by_m = a;
   sort_items(by_n, [](const OrthoItem& t) { return t.rows > t.cols ? t.rows : t.cols; });
   sort_items(by_m, [](const OrthoItem& t) { return t.rows < t.cols ? t.rows : t.cols; });
+  const OrthoTile gram = tile_of<kGram>(by_n), poly = tile_of<kPoly>(by_m), next = tile_of<kStep>(by_m);
   Coef c{(float)step.a, (float)step.b, (float)step.c, 0, false};
   for (int k = 0; k < step.steps; ++k) {
     c.last = k + 1 == step.steps;
     c.from = k & 1;
-    products_of<kGram>(by_n, f, step, c, s);
-    products_of<kPoly>(by_m, f, step, c, s);
-    if (c.last) products_of<kLast>(by_m, f, step, c, s);
-    else products_of<kStep>(by_m, f, step, c, s);
+    products_of<kGram>(by_n, gram, step, c, s);
+    products_of<kPoly>(by_m, poly, step, c, s);
+    if (c.last) products_of<kLast>(by_m, next, step, c, s);
+    else products_of<kStep>(by_m, next, step, c, s);
   }
   return hipGetLastError();
 }

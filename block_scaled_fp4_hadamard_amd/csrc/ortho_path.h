@@ -65,6 +65,66 @@ inline void each_ortho_group(const T* list, int32_t count, const Visit& visit) {
   if (n > 0) visit(at, n, bytes);
 }
 
+// How a product's result is cut into tiles, one for a workgroup: 64 to 256 a side; of 128 either one workgroup a CU with
+// three LDS stages or two with two.
+enum class OrthoTile { k64, k128, k128Two, k192, k256 };
+
+// What a tile costs (us): `start` for its first copies and its epilogue, and a step of 64 k, `alone` where few CUs work
+// and `shared` for a CU's part of a full chip, which power slows.  Fitted to 64 x 64 .. 4096 x 14336.
+struct OrthoCost {
+  OrthoTile tile;
+  int f, per;                                      // the tile's side in 64s, workgroups of a CU
+  double start, alone, shared;
+};
+constexpr OrthoCost kOrthoCosts[] = {{OrthoTile::k64, 1, 2, 4.0, 0.17, 0.25},
+                                     {OrthoTile::k128, 2, 1, 6.0, 0.30, 0.58},
+                                     {OrthoTile::k128Two, 2, 2, 6.0, 0.36, 0.56},
+                                     {OrthoTile::k192, 3, 1, 8.0, 0.52, 0.95},
+                                     {OrthoTile::k256, 4, 1, 14.0, 0.87, 1.55}};
+constexpr int kXcds = 8;
+constexpr int kCus = 256;
+
+// tiles of 64 f a side of a product's result: m x m of which those on and below the diagonal (sym), or m x n
+inline int64_t ortho_tiles(const OrthoSize& z, bool sym, int f) {
+  const int64_t tm = (z.m + 64 * f - 1) / (64 * f), tn = (z.n + 64 * f - 1) / (64 * f);
+  return sym ? tm * (tm + 1) / 2 : tm * tn;
+}
+
+// The time of one product of each of these matrices, longest K first, by the costs above: whole rounds of the chip, and
+// the rest, the shortest ones, in a last one.
+inline double ortho_time(const OrthoSize* sizes, int count, bool sym, bool gram, const OrthoCost& c) {
+  double tiles = 0.0, steps = 0.0;
+  for (int i = 0; i < count; ++i) {
+    const double n = (double)ortho_tiles(sizes[i], sym, c.f);
+    tiles += n;
+    steps += n * (double)((gram ? sizes[i].n : sizes[i].m) / 64);
+  }
+  const double longest = (double)((gram ? sizes[0].n : sizes[0].m) / 64);
+  const double shortest = (double)((gram ? sizes[count - 1].n : sizes[count - 1].m) / 64);
+  const double slots = (double)(kCus * c.per), rounds = floor(tiles / slots), rest = tiles - rounds * slots;
+  double us = rounds * c.start;
+  if (rounds > 0.0) us += (steps - rest * shortest) / kCus * c.shared;
+  if (rest > 0.0) {
+    const double k = rounds > 0.0 ? shortest : steps / tiles;
+    us += c.start + k * (c.alone + (c.per * c.shared - c.alone) * rest / slots);
+  }
+  const double least = c.start + longest * c.alone;
+  return us > least ? us : least;
+}
+
+inline OrthoTile ortho_choose(const OrthoSize* sizes, int count, bool sym, bool gram) {
+  OrthoTile best = OrthoTile::k64;
+  double least = 0.0;
+  for (const OrthoCost& c : kOrthoCosts) {
+    const double us = ortho_time(sizes, count, sym, gram, c);
+    if (&c == kOrthoCosts || us < least) {
+      best = c.tile;
+      least = us;
+    }
+  }
+  return best;
+}
+
 // The largest |p(s)|, p(s) = a s + b s^3 + c s^5, for 0 <= s <= top, and the largest |b t + c t^2| and |a + b t + c t^2|
 // for 0 <= t <= top^2: what bounds X, and the factors that multiply it, in the next step.
 struct OrthoReach {

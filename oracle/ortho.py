@@ -6,7 +6,7 @@ parts), with exact sums in between, and so says what that rounding costs on a gi
 import numpy as np
 
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
-SX, SF, LOW = 4096.0, 2048.0, 2048.0
+SX, SA = 4096.0, 2048.0
 
 
 def orthogonalize_ref(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
@@ -32,16 +32,16 @@ def orthogonalize_model(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
     x = x.T if tall else x
     x = x / (np.sqrt((x * x).sum()) + eps)
     hi = _half(x, SX)
-    low = _half(x - hi, SX * LOW)
+    low = _half(x - hi, SX)
     for k in range(steps):
-        s = _half(hi @ hi.T, SF)
+        s = _half(hi @ hi.T, SA)
         f = b * s + c * (s @ s)
         if k + 1 == steps:
-            x = _half(f + a * np.eye(len(f)), SF) @ hi
+            x = _half(f + a * np.eye(len(f)), 1.0) @ hi
         else:
-            x = a * (hi + low) + _half(f, SF) @ hi
+            x = a * (hi + low) + _half(f, 1.0) @ hi
             hi = _half(x, SX)
-            low = _half(x - hi, SX * LOW)
+            low = _half(x - hi, SX)
     return x.T if tall else x
 
 

@@ -52,7 +52,8 @@ struct View {
   int m, n;                              // shorter and longer side, in whole K steps
   int lm, ln;                            // and with room for any tile's rest
   double* parts;
-  half_t *x0, *x1, *low, *a, *b;         // x0 and x1 take turns
+  half_t *x0, *x1, *low;                 // x0 and x1 take turns
+  half_t *square;                        // three of [lm][lm]
 };
 
 __device__ __forceinline__ View view(const OrthoItem& t) {
@@ -67,8 +68,7 @@ __device__ __forceinline__ View view(const OrthoItem& t) {
   const int64_t mn = (int64_t)v.lm * v.ln;
   v.x1 = v.x0 + mn;
   v.low = v.x1 + mn;
-  v.a = v.low + mn;
-  v.b = v.a + (int64_t)v.lm * v.lm;
+  v.square = v.low + mn;
   return v;
 }
 
@@ -298,13 +298,14 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 // K advances 64 values (128 bytes of every row) a step, copied global -> LDS by
 // DMA into one of a ring of stages while another is consumed.
 //
-//   kGram  A = X X^T            both operands K-contiguous
-//   kPoly  B = b A + c A A      the same, A being its own transpose
-//   kStep  X' = a X + B X       the second operand has K as its rows: LDS reads
-//   kLast  O = B X              that transpose (ds_read_b64_tr_b16)
+//   kGram  A = X X^T              both operands K-contiguous
+//   kPoly  S = f S1 + g L R       the same: squares that are their own transposes
+//   kMix   S = f S1 + f2 S2 + g L R
+//   kStep  X' = x X + B X         the second operand has K as its rows: LDS reads
+//   kLast  O = B X                that transpose (ds_read_b64_tr_b16)
 //
-// A and B are symmetric: tiles on and below the diagonal are computed, and what
-// is below it is stored twice.
+// The squares are polynomials of A, hence symmetric, and commute: tiles on and
+// below the diagonal are computed, and what is below it is stored twice.
 //
 // Layout of the instruction: lane l holds row l % 32 of an operand and 8 of its
 // 16 k (8 (l / 32) ..); the 32 x 32 result has row 8 (r / 4) + 4 (l / 32) + r % 4 in
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 // .. + 7 and 16 more of its row (strip_col), so that a wave's 16-byte accesses
 // meet 32 bytes of each row.  For a tall matrix's last step the two sides change
 // places, so that the result leaves as the rows of O's transpose.
-enum Mode { kGram, kPoly, kStep, kLast };
+enum Mode { kGram, kPoly, kMix, kStep, kLast };
 
 // 16-byte piece's place in a 128-byte LDS row: a 16-byte LDS read serves the wave in groups of 16 lanes (0-3, 12-15 and
 // 20-27, and so on); with this order each group covers all 64 banks
@@ -400,14 +401,15 @@ __device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rat
 }
 
 struct Coef {
-  float a, b, c;
+  float x, f, f2, g;
+  float diagonal;                        // added to a square's diagonal
   int from;                              // which X holds the step's
-  bool last;
+  int left, right, add, add2, out;       // squares
 };
 
 template <int F, int S, int MODE, bool TRANS>
 __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a, const OrthoStep step, const Coef c) {
-  constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  constexpr bool kSym = MODE <= kMix;
   constexpr int T = 64 * F, kStage = T * kRow;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S * kStage];      // the first operand's stages, the second's
   uint8_t *const sP = lds, *const sQ = lds + S * kStage;
@@ -433,9 +435,11 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
   }
   const int m0 = ti * T, n0 = tj * T;
   const half_t* x = c.from ? v.x1 : v.x0;
-  const half_t* pp = MODE == kGram ? x : MODE == kPoly ? v.a : v.b;
-  const half_t* qq = MODE == kPoly ? v.a : x;
-  const int ldp = MODE == kGram ? v.ln : v.lm, ldq = MODE == kPoly ? v.lm : v.ln;
+  constexpr bool kSquares = MODE == kPoly || MODE == kMix;
+  const int64_t square = (int64_t)v.lm * v.lm;
+  const half_t* pp = MODE == kGram ? x : v.square + c.left * square;
+  const half_t* qq = kSquares ? v.square + c.right * square : x;
+  const int ldp = MODE == kGram ? v.ln : v.lm, ldq = kSquares ? v.lm : v.ln;
   const int nk = (MODE == kGram ? v.n : v.m) / 64;
 
   const int th = threadIdx.x, lane = th & 63, wave = __builtin_amdgcn_readfirstlane(th >> 6);
@@ -597,14 +601,20 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
     return TRANS ? n * ld + m : m * ld + n;
   };
   constexpr int kAhead = MODE == kGram ? 1 : MODE == kPoly ? 2 : 4;
+  half_t* const out = v.square + (kSym ? c.out * square : 0);
   u32x4 ahead[F < 3 ? F : 3][F][kAhead];
   auto ask = [&](int i, u32x4 (&to)[F][kAhead]) __attribute__((always_inline)) {
     each<F>([&](auto column) __attribute__((always_inline)) {
       constexpr int j = decltype(column)::value;
-      if constexpr (MODE == kPoly) {
-        const auto base = global(v.a + first_of(i, j)) + own;
+      if constexpr (kSquares) {
+        const auto base = global(v.square + c.add * square + first_of(i, j)) + own;
         to[j][0] = load_at<u32x4>(base);
         to[j][1] = load_at<u32x4>(base + 16);
+        if constexpr (MODE == kMix) {
+          const auto base2 = global(v.square + c.add2 * square + first_of(i, j)) + own;
+          to[j][2] = load_at<u32x4>(base2);
+          to[j][3] = load_at<u32x4>(base2 + 16);
+        }
       } else if constexpr (MODE == kStep) {
         const auto hi = global(x + first_of(i, j)) + own;
         const auto lo = global(v.low + first_of(i, j)) + own;
@@ -669,19 +679,21 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
           const int col = (TRANS ? m0 + wm + 32 * i : n0 + wn + 32 * j) + 16 * q + 8 * h;
           finish(t, keep, rate, row, col, first + 16 * q, own, o, w);
         } else if constexpr (kSym) {
-          half_t* out = MODE == kGram ? v.a : v.b;
           v8h y;
           if constexpr (MODE == kGram) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) y[r] = (half_t)(d[8 * q + r] * (kScaleA / (kScaleX * kScaleX)));
           } else {
             const v8h base = __builtin_bit_cast(v8h, got[j][q]);
+            v8h base2 = base;
+            if constexpr (MODE == kMix) base2 = __builtin_bit_cast(v8h, got[j][2 + q]);
             // the lane's row less its first column, where the diagonal may pass
             const int off = m0 + wm + 32 * i + l32 - (n0 + wn + 32 * j + 16 * q + 8 * h);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-              float o = fmaf(c.b / kScaleA, (float)base[r], d[8 * q + r] * (c.c / (kScaleA * kScaleA)));
-              if (c.last && off == r) o += c.a;
+              float o = fmaf(c.f, (float)base[r], d[8 * q + r] * c.g);
+              if constexpr (MODE == kMix) o = fmaf(c.f2, (float)base2[r], o);
+              if (off == r) o += c.diagonal;
               y[r] = (half_t)o;
             }
           }
@@ -692,7 +704,7 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
           v8h nh, nl;
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const float y = fmaf(c.a, (float)xl[r] + (float)xh[r], d[8 * q + r]);
+            const float y = fmaf(c.x, (float)xl[r] + (float)xh[r], d[8 * q + r]);
             nh[r] = (half_t)y;
             nl[r] = (half_t)(y - (float)nh[r]);
           }
@@ -705,7 +717,6 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
   });
   if constexpr (kSym) {
     if (ti == tj) return;
-    half_t* out = MODE == kGram ? v.a : v.b;
     const int s = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int n = 0; n < 32 * F; n += 16)
@@ -741,7 +752,7 @@ template <int F, int S, int MODE>
 void products(Args& a, const OrthoStep& step, const Coef& c, hipStream_t s) {
   const int total = deal(a, [&](const OrthoItem& t) {
     const OrthoSize z = ortho_size(t.rows, t.cols);
-    return (int)((ortho_tiles(z, MODE == kGram || MODE == kPoly, F) + kXcds - 1) / kXcds * kXcds);
+    return (int)((ortho_tiles(z, MODE <= kMix, F) + kXcds - 1) / kXcds * kXcds);
   });
   bool wide = MODE != kLast, tall = false;
   if (MODE == kLast)
@@ -757,7 +768,7 @@ template <int MODE>
 OrthoTile tile_of(const Args& a) {
   OrthoSize sizes[kOrthoGroup];
   for (int i = 0; i < a.count; ++i) sizes[i] = ortho_size(a.item[i].rows, a.item[i].cols);
-  return ortho_choose(sizes, a.count, MODE == kGram || MODE == kPoly, MODE == kGram);
+  return ortho_choose(sizes, a.count, MODE <= kMix, MODE == kGram);
 }
 
 template <int MODE>
@@ -789,13 +800,62 @@ hipError_t launch_ortho(const OrthoItem* items, int count, const OrthoStep& step
   sort_items(by_n, [](const OrthoItem& t) { return t.rows > t.cols ? t.rows : t.cols; });
   sort_items(by_m, [](const OrthoItem& t) { return t.rows < t.cols ? t.rows : t.cols; });
   const OrthoTile gram = tile_of<kGram>(by_n), poly = tile_of<kPoly>(by_m), next = tile_of<kStep>(by_m);
-  Coef c{(float)step.a, (float)step.b, (float)step.c, 0, false};
-  for (int k = 0; k < step.steps; ++k) {
-    c.last = k + 1 == step.steps;
-    c.from = k & 1;
+  Coef c{};
+  auto gram_of_x = [&](int from) {
+    c.from = from;
+    c.out = 0;
     products_of<kGram>(by_n, gram, step, c, s);
+  };
+  // out = b A + c A A, and a on its diagonal if asked for
+  auto poly_of = [&](int of, int out, double diagonal) {
+    c.left = c.right = c.add = of;
+    c.out = out;
+    c.f = (float)(step.b / kScaleA);
+    c.g = (float)(step.c / ((double)kScaleA * kScaleA));
+    c.diagonal = (float)diagonal;
     products_of<kPoly>(by_m, poly, step, c, s);
-    if (c.last) products_of<kLast>(by_m, next, step, c, s);
+    c.diagonal = 0.0f;
+  };
+  // out = f S + L R
+  auto times = [&](double f, int add, int left, int right, int out) {
+    c.f = (float)f;
+    c.g = 1.0f;
+    c.add = add;
+    c.left = left;
+    c.right = right;
+    c.out = out;
+    products_of<kPoly>(by_m, poly, step, c, s);
+  };
+  int k = 0, from = 0;
+  // The first two steps in one, where the list's matrices are wide: with P0 = a I + B0 and P1 = a I + B1 their factors, X2
+  // = P1 P0 X0, and A1 = P0 A0 P0 comes from squares instead of a second pass over X.  That trades 3 m^2 n products for 3
+  // m^3 and a pass of X; the roundings of A1's detour are no larger than those of X1 X1^T.  (Three steps in one lose
+  // weak directions: 4e-3 off on a matrix of rank 1.)
+  if (step.steps >= 3 && ortho_joins(by_m.item, count)) {
+    gram_of_x(0);                                    // 0: A0
+    poly_of(0, 1, 0.0);                              // 1: B0
+    times(step.a, 0, 1, 0, 2);                       // 2: P0 A0
+    times(step.a, 2, 1, 2, 0);                       // 0: A1 = P0 (P0 A0)
+    poly_of(0, 2, 0.0);                              // 2: B1
+    c.f = c.f2 = (float)step.a;                      // 0: P1 P0 - a^2 I = a B0 + a B1 + B1 B0
+    c.g = 1.0f;
+    c.add = c.left = 1;
+    c.add2 = c.right = 2;
+    c.out = 0;
+    products_of<kMix>(by_m, poly, step, c, s);
+    c.left = 0;
+    c.x = (float)(step.a * step.a);
+    products_of<kStep>(by_m, next, step, c, s);
+    k = 2;
+    from = 1;
+  }
+  for (; k < step.steps; ++k, from ^= 1) {
+    const bool last = k + 1 == step.steps;
+    gram_of_x(from);
+    poly_of(0, 1, last ? step.a : 0.0);
+    c.left = 1;
+    c.x = (float)step.a;
+    if (last) products_of<kLast>(by_m, next, step, c, s);
     else products_of<kStep>(by_m, next, step, c, s);
   }
   return hipGetLastError();

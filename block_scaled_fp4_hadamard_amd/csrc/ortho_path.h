@@ -20,7 +20,7 @@ constexpr int64_t kOrthoRun = 8192;                // elements for each of them 
 inline int64_t ortho_pad(int64_t n) { return (n + kOrthoPad - 1) / kOrthoPad * kOrthoPad; }
 
 // A matrix's place in the workspace, in bytes: the sums of squares (float64), then X, the next X and X's low part
-// [m][n], A and B [m][m] in float16; m the shorter side, n the longer, each with room for a tile's rest.  (The rest also
+// [m][n], and three squares [m][m] in float16; m the shorter side, n the longer, each with room for a tile's rest.  (The rest also
 // keeps the rows of a matrix whose sides are powers of two out of step with the memory's channels.)
 struct OrthoSize {
   int64_t m, n;                                    // in whole K steps
@@ -35,7 +35,7 @@ inline OrthoSize ortho_size(int64_t rows, int64_t cols) {
   s.parts = (rows * cols + kOrthoRun - 1) / kOrthoRun;
   if (s.parts > kOrthoParts) s.parts = kOrthoParts;
   const int64_t lm = s.m + kOrthoRest, ln = s.n + kOrthoRest;
-  s.bytes = 8 * kOrthoParts + 2 * (3 * lm * ln + 2 * lm * lm);
+  s.bytes = 8 * kOrthoParts + 2 * (3 * lm * ln + 3 * lm * lm);
   return s;
 }
 
@@ -123,6 +123,20 @@ inline OrthoTile ortho_choose(const OrthoSize* sizes, int count, bool sym, bool 
     }
   }
   return best;
+}
+
+// Whether the first two steps of these matrices run as one: it replaces 3 m^2 n multiplications by 3 m^3 (symmetric
+// products counted half) and saves a pass of X, for one launch more, which large products do not notice.  4096 x 14336:
+// 4.27 ms against 4.83; 4096 x 4096: 1.36 against 1.34.
+template <typename T>
+inline bool ortho_joins(const T* list, int count) {
+  double wide = 0.0, square = 0.0;
+  for (int i = 0; i < count; ++i) {
+    const OrthoSize z = ortho_size(list[i].rows, list[i].cols);
+    wide += (double)z.m * z.m * z.n;
+    square += (double)z.m * z.m * z.m;
+  }
+  return wide >= 1.25 * square && wide >= 4e9;
 }
 
 // The largest |p(s)|, p(s) = a s + b s^3 + c s^5, for 0 <= s <= top, and the largest |b t + c t^2| and |a + b t + c t^2|

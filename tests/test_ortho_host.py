@@ -96,12 +96,12 @@ def test_workspace_and_groups():
 
     one = need((100, 300))
     # 100 and 300 in whole steps of 64, and 192 more for a tile's rest
-    assert one == 8 * 256 + 2 * (3 * 320 * 512 + 2 * 320 * 320) == need((300, 100))
+    assert one == 8 * 256 + 2 * (3 * 320 * 512 + 3 * 320 * 320) == need((300, 100))
     assert need((100, 300), (0, 5), (100, 300)) == 2 * one
     assert need(*[(100, 300)] * 40) == 32 * one                     # 32 matrices are worked on at a time
     # and within 2 GiB
     assert need(*[(8192, 16384)] * 3) == need((8192, 16384)) > 1 << 30
-    assert need(*[(8000, 15744)] * 3) == 2 * need((8000, 15744)) < 1 << 31
+    assert need(*[(6400, 15744)] * 3) == 2 * need((6400, 15744)) < 1 << 31
     assert need((40000, 60000)) > 1 << 33                          # but one matrix whatever its size
     assert need() == need((0, 3)) == need((1 << 20, 5)) == need((1 << 16, 1 << 16)) == need((-1, 5)) == 0
     assert ask(None, 3) == 0 and ask(None, -1) == 0

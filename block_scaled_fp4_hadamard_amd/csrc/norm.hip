@@ -108,6 +108,21 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf16, float none
   }
 }
 
+// a pointer that is the same in all lanes of a wave
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (T*)(((uint64_t)hi << 32) | lo);
+}
+// row `row` of a matrix, uniform where a wave has one row (G lanes a row)
+template <int G, typename T>
+__device__ __forceinline__ T* row_of(T* p, int64_t row, int64_t ld) {
+  if constexpr (G >= 64) return uniform(p + row * ld);
+  else return p + row * ld;
+}
+
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
@@ -257,18 +272,19 @@ __global__ void __launch_bounds__(1024) norm_wide(const NormParams p, const bool
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  One workgroup of 1024 lanes a CU at most, of kRows = 1024 / G rows
-// at a time; a lane keeps its columns' sums of dy and dy * h over all its rows
+// Backward.  One workgroup of 1024 lanes a CU at most (few rows: of 256), of
+// kRows = THREADS / G rows at a time; a lane keeps its columns' sums of dy and dy * h over all its rows
 // in registers.  At the end the workgroup's rows are added in LDS, one after
 // another, and its sums go to the workspace; norm_grad_sum adds the workgroups'
 // in order.
-constexpr int kGradThreads = 1024;
 constexpr int kGradGrid = 256;
+constexpr int kLong = 19456;             // columns whose two sums fit into LDS
+constexpr int kLongLanes = 512;          // 1024 leave 128 registers a lane, too few for two rows
 
-template <typename T, int KIND, int G, int N>
-__global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const NormGradParams p, const bool wbf, float* parts) {
-  constexpr int E = kPer<T>, kRows = kGradThreads / G, kCols = G * N * E;
-  __shared__ float red[2][2][kGradThreads / 64];
+template <typename T, int KIND, int G, int N, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradParams p, const bool wbf, float* parts) {
+  constexpr int E = kPer<T>, kRows = THREADS / G, kCols = G * N * E;
+  __shared__ float red[2][2][THREADS / 64];
   __shared__ float sum[kRows > 1 ? 2 * kCols : 1];
   const int lane = threadIdx.x % G, mine = threadIdx.x / G, wave = threadIdx.x / 64, cols = (int)p.cols;
   const int first = mine * (G / 64);              // the row's first wave (G > 64)
@@ -278,29 +294,45 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const NormGradP
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.0f;
+  // the lane's weights: a load of theirs in the loop would wait for the row asked for before it
+  float w[N][E];
+#pragma unroll
+  for (int i = 0; i < N; ++i) load_weight<E>(p.weight, wbf, 1.0f, (i * G + lane) * E, cols, w[i]);
   int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.rows; base += (int64_t)gridDim.x * kRows, turn ^= 1) {
-    const int64_t row = base + mine;
+  // a row, asked for while the one before it is worked on
+  struct Row {
+    u32x4 x[N], dy[N];
+    float mean, rstd;
+  };
+  auto ask = [&](int64_t row, Row& r) {
     const bool real = row < p.rows;
-    const T* x = (const T*)p.x + row * p.ld_x;
-    const T* dy = (const T*)p.dy + row * p.ld_dy;
-    u32x4 rx[N], ry[N];
+    const T* x = row_of<G>((const T*)p.x, row, p.ld_x);
+    const T* dy = row_of<G>((const T*)p.dy, row, p.ld_dy);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      rx[i] = load_raw(x, (i * G + lane) * E, real ? cols : 0);
-      ry[i] = load_raw(dy, (i * G + lane) * E, real ? cols : 0);
+      r.x[i] = load_raw(x, (i * G + lane) * E, real ? cols : 0);
+      r.dy[i] = load_raw(dy, (i * G + lane) * E, real ? cols : 0);
     }
-    const float mean = KIND == MX_NORM_LAYER && real ? p.mean[row] : 0.0f;
-    const float rstd = real ? p.rstd[row] : 0.0f;
+    r.mean = KIND == MX_NORM_LAYER && real ? p.mean[row] : 0.0f;
+    r.rstd = real ? p.rstd[row] : 0.0f;
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  Row ahead;
+  ask((int64_t)blockIdx.x * kRows + mine, ahead);
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.rows; base += step, turn ^= 1) {
+    const int64_t row = base + mine;
+    const bool real = row < p.rows;
+    const Row now = ahead;
+    ask(row + step, ahead);
+    const auto &rx = now.x, &ry = now.dy;
+    const float mean = now.mean, rstd = now.rstd;
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float w[E];
-      load_weight<E>(p.weight, wbf, 1.0f, (i * G + lane) * E, cols, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         // past the row's end dy is zero
-        const float h = (part<T>(rx[i], e) - mean) * rstd, d = part<T>(ry[i], e), g = d * w[e];
+        const float h = (part<T>(rx[i], e) - mean) * rstd, d = part<T>(ry[i], e), g = d * w[i][e];
         c1 += g;
         c2 = fmaf(g, h, c2);
         dw[i][e] = fmaf(d, h, dw[i][e]);
@@ -331,17 +363,16 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const NormGradP
     c1 = KIND == MX_NORM_LAYER ? c1 / n : 0.0f;
     c2 /= n;
     if (!real) continue;
-    T* dx = (T*)p.dx + row * p.ld_dx;
+    T* dx = row_of<G>((T*)p.dx, row, p.ld_dx);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = (i * G + lane) * E;
       if (at >= cols) continue;
-      float w[E], o[E];
-      load_weight<E>(p.weight, wbf, 1.0f, at, cols, w);
+      float o[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float h = (part<T>(rx[i], e) - mean) * rstd;
-        o[e] = (fmaf(part<T>(ry[i], e), w[e], -c1) - h * c2) * rstd;
+        o[e] = (fmaf(part<T>(ry[i], e), w[i][e], -c1) - h * c2) * rstd;
       }
       store(dx, at, cols, o);
     }
@@ -374,14 +405,107 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const NormGradP
       }
       __syncthreads();
     }
-    for (int at = threadIdx.x; at < cols; at += kGradThreads) {
+    for (int at = threadIdx.x; at < cols; at += THREADS) {
       out[at] = sum[at];
       out[cols + at] = sum[kCols + at];
     }
   }
 }
 
-// Wide rows: the two sums of every row first, then columns in strips, each lane one column over a run of rows.
+// Long rows: one workgroup of 512 lanes takes a row at a time, the next one asked for ahead; the columns' sums live in
+// LDS, each lane adding to its own, so that registers hold the rows.
+template <typename T, int KIND, int N>
+__global__ void __launch_bounds__(kLongLanes) norm_grad_long(const NormGradParams p, const bool wbf, float* parts) {
+  constexpr int E = kPer<T>;
+  __shared__ float red[2][2][kLongLanes / 64];
+  __shared__ __attribute__((aligned(16))) float sum[2][kLong];
+  typedef float v4f __attribute__((ext_vector_type(4)));
+  const int lane = threadIdx.x, wave = lane / 64, cols = (int)p.cols;
+  const float n = (float)cols;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int q = 0; q < E; q += 4) {
+      const int at = (i * kLongLanes + lane) * E + q;
+      if (at < cols) *(v4f*)&sum[0][at] = *(v4f*)&sum[1][at] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+  float w[N][E];
+#pragma unroll
+  for (int i = 0; i < N; ++i) load_weight<E>(p.weight, wbf, 1.0f, (i * kLongLanes + lane) * E, cols, w[i]);
+  struct Row {
+    u32x4 x[N], dy[N];
+    float mean, rstd;
+  };
+  auto ask = [&](int64_t row, Row& r) {
+    const bool real = row < p.rows;
+    const T* x = row_of<kLongLanes>((const T*)p.x, row, p.ld_x);
+    const T* dy = row_of<kLongLanes>((const T*)p.dy, row, p.ld_dy);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      r.x[i] = load_raw(x, (i * kLongLanes + lane) * E, real ? cols : 0);
+      r.dy[i] = load_raw(dy, (i * kLongLanes + lane) * E, real ? cols : 0);
+    }
+    r.mean = KIND == MX_NORM_LAYER && real ? p.mean[row] : 0.0f;
+    r.rstd = real ? p.rstd[row] : 0.0f;
+  };
+  Row ahead;
+  ask(blockIdx.x, ahead);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const Row now = ahead;
+    ask(row + gridDim.x, ahead);
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (i * kLongLanes + lane) * E;
+      if (at >= cols) continue;
+#pragma unroll
+      for (int q = 0; q < E; q += 4) {
+        v4f a = *(const v4f*)&sum[0][at + q], b = *(const v4f*)&sum[1][at + q];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float h = (part<T>(now.x[i], q + e) - now.mean) * now.rstd, d = part<T>(now.dy[i], q + e), g = d * w[i][q + e];
+          c1 += g;
+          c2 = fmaf(g, h, c2);
+          a[e] = fmaf(d, h, a[e]);
+          b[e] += d;
+        }
+        *(v4f*)&sum[0][at + q] = a;
+        *(v4f*)&sum[1][at + q] = b;
+      }
+    }
+    c1 = row_sum<kLongLanes>(c1, red[turn][0], wave, 0);
+    c2 = row_sum<kLongLanes>(c2, red[turn][1], wave, 0) / n;
+    c1 = KIND == MX_NORM_LAYER ? c1 / n : 0.0f;
+    T* dx = row_of<kLongLanes>((T*)p.dx, row, p.ld_dx);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (i * kLongLanes + lane) * E;
+      if (at >= cols) continue;
+      float o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float h = (part<T>(now.x[i], e) - now.mean) * now.rstd;
+        o[e] = (fmaf(part<T>(now.dy[i], e), w[i][e], -c1) - h * c2) * now.rstd;
+      }
+      store(dx, at, cols, o);
+    }
+  }
+  if (parts == nullptr) return;
+  float* out = parts + (int64_t)blockIdx.x * 2 * p.cols;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int at = (i * kLongLanes + lane) * E + e;
+      if (at < cols) {
+        out[at] = sum[0][at];
+        out[cols + at] = sum[1][at];
+      }
+    }
+}
+
+// Wider rows: the two sums of every row first, then columns in strips, each lane one column over a run of rows.
 template <typename T, int KIND>
 __global__ void __launch_bounds__(1024) norm_grad_wide_rows(const NormGradParams p, const bool wbf, float* c) {
   constexpr int E = kPer<T>;
@@ -462,49 +586,53 @@ __global__ void __launch_bounds__(1024) norm_grad_sum(const float* parts, int co
 }
 
 struct Shape {
-  int lanes, vectors;            // G and N; lanes 0: wide rows
+  int lanes, vectors;            // G and N; lanes 0: rows wider than registers
+  int threads;                   // of a workgroup
 };
 
-// The lanes of a row, for `cols` elements of E a vector, and `most` vectors a lane at most.
-Shape forward_shape(int64_t cols, int64_t rows, int e) {
+// The lanes of a row, for `cols` elements of e a vector.
+Shape forward_shape(int64_t cols, int e) {
   const int64_t v = (cols + e - 1) / e;
-  if (v <= 16) return {16, 1};
-  if (v <= 32) return {16, 2};
-  if (v <= 64) return {64, 1};
-  if (v <= 128) return {64, 2};
-  if (v <= 256) return {256, 1};
-  if (v <= 512) return {256, 2};
-  if (v <= 1024) return {256, 4};
-  if (v <= 2048) return {1024, 2};
-  if (v <= 4096) return {1024, 4};
-  return {0, 0};
+  if (v <= 16) return {16, 1, 256};
+  if (v <= 32) return {16, 2, 256};
+  if (v <= 64) return {64, 1, 256};
+  if (v <= 128) return {64, 2, 256};
+  if (v <= 256) return {256, 1, 256};
+  if (v <= 512) return {256, 2, 256};
+  if (v <= 1024) return {256, 4, 256};
+  if (v <= 1536) return {256, 6, 256};
+  if (v <= 2048) return {256, 8, 256};
+  if (v <= 4096) return {1024, 4, 1024};
+  return {0, 0, 1024};
 }
 
-Shape grad_shape(int64_t cols, int e) {
+// Backward.  Few rows take small workgroups, so that more CUs share them (33 x 4096: 5.4 us for 9.0); many take large
+// ones, of which each leaves its sums once.
+Shape grad_shape(int64_t cols, int64_t rows, int e) {
   const int64_t v = (cols + e - 1) / e;
-  if (v <= 16) return {16, 1};
-  if (v <= 32) return {16, 2};
-  if (v <= 64) return {64, 1};
-  if (v <= 128) return {64, 2};
-  if (v <= 256) return {256, 1};
-  if (v <= 512) return {256, 2};
-  if (v <= 1024) return {1024, 1};
-  if (v <= 2048) return {1024, 2};
-  return {0, 0};
+  Shape s = {0, 0, 1024};
+  if (v <= 32) s = {16, v <= 16 ? 1 : 2, 1024};
+  else if (v <= 128) s = {64, v <= 64 ? 1 : 2, 1024};
+  else if (v <= 512) s = {256, v <= 256 ? 1 : 2, 1024};
+  else if (v <= 1024) return {1024, 1, 1024};
+  else if (v <= 2048 && e == 4) return {1024, 2, 1024};
+  else if (cols <= kLong) return {kLongLanes, (int)((v + 2 * kLongLanes - 1) / (2 * kLongLanes)) * 2, kLongLanes};
+  if (s.lanes != 0 && rows <= kGradGrid * (256 / s.lanes)) s.threads = 256;
+  return s;
 }
 
-constexpr int64_t kWideRuns = 256;                // runs of rows of the wide kernel at most
+constexpr int64_t kWideRuns = 256;                // runs of rows of the kernels for the widest rows at most
 
 // workgroups whose sums the workspace holds
 int64_t grad_parts(int64_t rows, const Shape& s) {
   if (s.lanes == 0) return rows < kWideRuns ? rows : kWideRuns;
-  const int64_t each = kGradThreads / s.lanes, need = (rows + each - 1) / each;
+  const int64_t each = s.threads / s.lanes, need = (rows + each - 1) / each;
   return need < kGradGrid ? need : kGradGrid;
 }
 
 template <typename T, int KIND>
 hipError_t forward(const NormParams& p, bool wbf, hipStream_t st) {
-  const Shape s = forward_shape(p.cols, p.rows, kPer<T>);
+  const Shape s = forward_shape(p.cols, kPer<T>);
   const int64_t each = s.lanes == 0 || s.lanes >= 256 ? 1 : 256 / s.lanes, need = (p.rows + each - 1) / each;
   const int64_t most = s.lanes == 0 || s.lanes == 1024 ? kGrid / 4 : kGrid;
   const dim3 g((unsigned)(need < most ? need : most));
@@ -514,7 +642,7 @@ hipError_t forward(const NormParams& p, bool wbf, hipStream_t st) {
     return hipGetLastError();                                                                                   \
   }
   MX_NORM_CASE(16, 1) MX_NORM_CASE(16, 2) MX_NORM_CASE(64, 1) MX_NORM_CASE(64, 2) MX_NORM_CASE(256, 1)
-  MX_NORM_CASE(256, 2) MX_NORM_CASE(256, 4) MX_NORM_CASE(1024, 2) MX_NORM_CASE(1024, 4)
+  MX_NORM_CASE(256, 2) MX_NORM_CASE(256, 4) MX_NORM_CASE(256, 6) MX_NORM_CASE(256, 8) MX_NORM_CASE(1024, 4)
 #undef MX_NORM_CASE
   hipLaunchKernelGGL((norm_wide<T, KIND>), g, dim3(1024), 0, st, p, wbf);
   return hipGetLastError();
@@ -523,15 +651,30 @@ hipError_t forward(const NormParams& p, bool wbf, hipStream_t st) {
 template <typename T, int KIND>
 hipError_t backward(const NormGradParams& p, bool wbf, float* ws, hipStream_t st) {
   const bool sums = p.dweight != nullptr || p.dbias != nullptr;
-  const Shape s = grad_shape(p.cols, kPer<T>);
+  const Shape s = grad_shape(p.cols, p.rows, kPer<T>);
   const int64_t count = grad_parts(p.rows, s);       // 0 without rows: the sums are zeros
   float* parts = sums ? ws : nullptr;
   const dim3 g((unsigned)count);
-#define MX_NORM_CASE(LANES, VECTORS)                                                                         \
-  if (count > 0 && s.lanes == LANES && s.vectors == VECTORS)                                                 \
-    hipLaunchKernelGGL((norm_grad_kernel<T, KIND, LANES, VECTORS>), g, dim3(kGradThreads), 0, st, p, wbf, parts);
-  MX_NORM_CASE(16, 1) MX_NORM_CASE(16, 2) MX_NORM_CASE(64, 1) MX_NORM_CASE(64, 2) MX_NORM_CASE(256, 1)
-  MX_NORM_CASE(256, 2) MX_NORM_CASE(1024, 1) MX_NORM_CASE(1024, 2)
+#define MX_NORM_CASE(LANES, VECTORS, THREADS)                                                                         \
+  if (count > 0 && s.lanes == LANES && s.vectors == VECTORS && s.threads == THREADS)                                  \
+    hipLaunchKernelGGL((norm_grad_kernel<T, KIND, LANES, VECTORS, THREADS>), g, dim3(THREADS), 0, st, p, wbf, parts);
+  MX_NORM_CASE(16, 1, 256) MX_NORM_CASE(16, 2, 256) MX_NORM_CASE(64, 1, 256) MX_NORM_CASE(64, 2, 256)
+  MX_NORM_CASE(256, 1, 256) MX_NORM_CASE(256, 2, 256) MX_NORM_CASE(16, 1, 1024) MX_NORM_CASE(16, 2, 1024)
+  MX_NORM_CASE(64, 1, 1024) MX_NORM_CASE(64, 2, 1024) MX_NORM_CASE(256, 1, 1024) MX_NORM_CASE(256, 2, 1024)
+  MX_NORM_CASE(1024, 1, 1024)
+  if constexpr (sizeof(T) == 4) {
+    MX_NORM_CASE(1024, 2, 1024)
+  }
+#undef MX_NORM_CASE
+#define MX_NORM_CASE(VECTORS)                                                                                      \
+  if (count > 0 && s.lanes == kLongLanes && s.vectors == VECTORS)                                                  \
+    hipLaunchKernelGGL((norm_grad_long<T, KIND, VECTORS>), g, dim3(kLongLanes), 0, st, p, wbf, parts);
+  MX_NORM_CASE(6)
+  if constexpr (sizeof(T) == 4) {
+    MX_NORM_CASE(8) MX_NORM_CASE(10)
+  } else {
+    MX_NORM_CASE(4)
+  }
 #undef MX_NORM_CASE
   if (count > 0 && s.lanes == 0) {
     float* c = sums ? ws + 2 * count * p.cols : ws;
@@ -557,7 +700,7 @@ hipError_t launch_norm(const NormParams& p, int type, int weight_type, int kind,
 }
 
 int64_t norm_grad_workspace(int64_t rows, int64_t cols, int type, bool sums) {
-  const Shape s = grad_shape(cols, type == MX_OUT_BF16 ? 8 : 4);
+  const Shape s = grad_shape(cols, rows, type == MX_OUT_BF16 ? 8 : 4);
   return 4 * ((sums ? 2 * grad_parts(rows, s) * cols : 0) + (s.lanes == 0 ? 2 * rows : 0));
 }
 

@@ -167,6 +167,22 @@ __device__ __forceinline__ void load_gradient(const OrthoItem& t, int64_t at, in
   for (int e = 0; e < N; ++e) o[e] *= scale;
 }
 
+__device__ __forceinline__ void load_gradient(const OrthoItem& t, int64_t at, float scale, float& o) {
+  o = (t.g_bf16 ? bf16_value(((const uint16_t*)t.g)[at]) : ((const float*)t.g)[at]) * scale;
+}
+
+// U's scale 2^12 / (|U| + eps), whose float32 might overflow or sink, in two factors
+struct Scale {
+  float factor;
+  int power;
+};
+__device__ __forceinline__ Scale scale_of(double sum, double eps) {
+  int power;
+  const double f = frexp((double)kScaleX / (sqrt(sum) + eps), &power);
+  return Scale{(float)f, power};
+}
+__device__ __forceinline__ float scaled(float u, const Scale& s) { return ldexpf(u * s.factor, s.power); }
+
 constexpr int kSumThreads = 1024;
 
 __global__ void __launch_bounds__(kSumThreads) ortho_sum(const Args a, const OrthoStep step) {
@@ -258,7 +274,7 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
   sum = (red[0] + red[1]) + (red[2] + red[3]);
-  const double scale = (double)kScaleX / (sqrt(sum) + step.eps);
+  const Scale scale = scale_of(sum, step.eps);
   auto put = [&](int m, int n, const float (&x)[4]) {
     v4h hi, lo;
 #pragma unroll
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u[i][e] = (float)((double)u[i][e] * scale);
+    for (int e = 0; e < 4; ++e) u[i][e] = scaled(u[i][e], scale);
     if (!tall) {
       put(row + 16 * i, col, u[i]);
     } else {
@@ -398,6 +414,16 @@ __device__ __forceinline__ void finish(const OrthoItem& t, float keep, float rat
         else out32[e] = o[e];
       }
   }
+}
+
+// what the weights keep, and what they take of the result
+__device__ __forceinline__ void rates(const OrthoItem& t, const OrthoStep& step, float& keep, float& rate) {
+  keep = 1.0f;
+  rate = 0.0f;
+  if (t.w == nullptr) return;
+  const double lr = step.lr_dev ? (double)*step.lr_dev : step.lr;
+  keep = (float)(1.0 - lr * step.weight_decay);
+  rate = (float)(lr * t.scale);
 }
 
 struct Coef {
@@ -582,13 +608,7 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
     st = next;
   };
   float keep = 1.0f, rate = 0.0f;
-  if constexpr (MODE == kLast) {
-    if (t.w != nullptr) {
-      const double lr = step.lr_dev ? (double)*step.lr_dev : step.lr;
-      keep = (float)(1.0 - lr * step.weight_decay);
-      rate = (float)(lr * t.scale);
-    }
-  }
+  if constexpr (MODE == kLast) rates(t, step, keep, rate);
   // The epilogue, a row of fragments at a time; what it reads is asked for two rows ahead, the first two before the last
   // step's products.  TRANS: the lane's column is l % 32 of strip j, its rows 8 h .. and 16 + 8 h .. of strip i.  In the
   // result's own rows a lane is always at row l % 32 and columns 8 h .. of a fragment: one offset a lane, and a uniform
@@ -730,6 +750,284 @@ __global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a
   }
 }
 
+// ---------------------------------------------------------------------------
+// Small matrices: a workgroup of sixteen waves takes one through all of its steps
+// in LDS: X (its low part in registers, where the last product left it), A and
+// B.  What a launch for each product costs (3 to 4 us each, 17 of them) is more
+// than the work.  The rows of all three are an odd number of 16 bytes apart, so
+// that row reads and transposing reads part the banks.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+
+constexpr int NF = 2;                      // fragments of X a wave has at most
+
+__global__ void __launch_bounds__(kSmallThreads) ortho_small(const Args a, const OrthoStep step) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t mem[];
+  const OrthoItem t = a.item[blockIdx.x];
+  const View v = view(t);
+  const Moment c = moment_of(step);
+  const int px = ortho_pitch(v.n), ps = ortho_pitch(v.m);        // bytes between rows
+  uint8_t *const sX = mem, *const sA = sX + v.m * px, *const sB = sA + v.m * ps;
+  // U and the result, [m][n] in float32, before and after the others
+  float* const whole = (float*)mem;
+  const int pw = v.n + 4;
+  __shared__ double red[kSmallThreads / 64];
+  const int th = threadIdx.x, lane = th & 63, wave = __builtin_amdgcn_readfirstlane(th >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const bool tall = t.rows > t.cols;
+  const int fm = v.m / 32, fms = fm == 4 ? 2 : 1, frags = fm * (v.n / 32);       // v.m is 64 or 128
+  // fragment f of the wave: strips (i, j) of X; a lane has row l % 32 and columns 8 h .. and 16 + 8 h ..
+  auto strips = [&](int f, int& i, int& j) {
+    const int k = wave + kSmallWaves * f;
+    i = k & (fm - 1);
+    j = k >> fms;
+    return k < frags;
+  };
+  // U in pieces of four neighbouring values: a wave takes as many rows at a time as 64 lanes hold, kAtOnce times
+  const int pieces = (t.cols + 3) / 4, shift = pieces > 32 ? 6 : pieces > 1 ? 32 - __builtin_clz(pieces - 1) : 0, across = 1 << shift;
+  const int rows_at_once = 64 >> shift, lane_row = lane >> shift, lane_col = 4 * (lane & (across - 1));
+  constexpr int kAtOnce = 4;
+  // begin(e, row, column) for the lane's pieces of a batch, which asks for what they need, then end(e, row, column)
+  auto batches = [&](auto begin, auto end) {
+#pragma unroll 1
+    for (int col = lane_col; col - lane_col < t.cols; col += 256)
+#pragma unroll 1
+      for (int from = wave * rows_at_once; from < t.rows; from += kSmallWaves * kAtOnce * rows_at_once) {
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) begin(e, from + kSmallWaves * e * rows_at_once + lane_row, col);
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) end(e, from + kSmallWaves * e * rows_at_once + lane_row, col);
+      }
+  };
+  auto count_of = [&](int row, int col) { return row < t.rows ? min(4, t.cols - col) : 0; };
+
+  for (int i = th; i < v.m * pw / 4; i += kSmallThreads) ((v4f*)whole)[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  double sum = 0.0;
+  {
+#pragma clang fp contract(off)
+    float u[kAtOnce][4], x[kAtOnce][4];
+    batches(
+        [&](int e, int row, int col) {
+          const int count = count_of(row, col);
+          if (count <= 0) return;
+          load_gradient(t, (int64_t)row * t.ld_g + col, count, c.scale, u[e]);
+          if (t.moment != nullptr) load_values(t.moment + row * t.cols + col, count, x[e]);
+        },
+        [&](int e, int row, int col) {
+          const int count = count_of(row, col);
+          if (count <= 0) return;
+          if (t.moment != nullptr) {
+            float* to = t.moment + row * t.cols + col;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[e][k] = x[e][k] * c.mu + u[e][k] * c.rest;
+              if (k < count) to[k] = x[e][k];
+              u[e][k] = update_of(u[e][k], x[e][k], c);
+            }
+          }
+          if (tall) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < count) whole[(col + k) * pw + row] = u[e][k];
+          } else {
+            // past the last column these are zeros, and inside the padded row
+            *(v4f*)(whole + row * pw + col) = v4f{u[e][0], u[e][1], u[e][2], u[e][3]};
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum += (double)u[e][k] * (double)u[e][k];
+        });
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if (lane == 0) red[wave] = sum;
+  __syncthreads();
+  sum = red[0];
+#pragma unroll
+  for (int i = 1; i < kSmallThreads / 64; ++i) sum += red[i];
+  const Scale scale = scale_of(sum, step.eps);
+
+  v8h high[NF][2], low[NF][2];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    int i, j;
+    if (!strips(f, i, j)) continue;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const v4f* u = (const v4f*)(whole + (32 * i + l32) * pw + 32 * j + 16 * q + 8 * h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = scaled(u[e / 4][e % 4], scale);
+        high[f][q][e] = (half_t)x;
+        low[f][q][e] = (half_t)(x - (float)high[f][q][e]);
+      }
+    }
+  }
+  auto keep_x = [&]() {
+    __syncthreads();                         // what X takes the place of has been read
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      int i, j;
+      if (!strips(f, i, j)) continue;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) *(v8h*)(sX + (32 * i + l32) * px + 2 * (32 * j + 16 * q + 8 * h)) = high[f][q];
+    }
+    __syncthreads();
+  };
+
+  const int order = strip_col(l32);
+  const int chunk = strip_col(4 * (4 * ((lane >> 4) & 1) + (lane & 3))), krow = 8 * h + ((lane >> 2) & 3);
+  // strip i of a matrix as the second operand, strip j as the first, 16 k from 16 s on
+  auto rows_of = [&](const uint8_t* x, int pitch, int i, int s) {
+    return *(const v8h*)(x + (32 * i + l32) * pitch + 32 * s + 16 * h);
+  };
+  auto strip_of = [&](const uint8_t* x, int pitch, int j, int s) {
+    return *(const v8h*)(x + (32 * j + order) * pitch + 32 * s + 16 * h);
+  };
+  auto columns_of = [&](const uint8_t* x, int pitch, int j, int s) {
+    const uint8_t* p = x + (16 * s + krow) * pitch + 2 * (32 * j + chunk);
+    return read_columns(p, p + 4 * pitch);
+  };
+  const v16f zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // A wave's fragments lie in one strip of rows, since the waves are a multiple of the strips: they share the second
+  // operand, and their products are independent of one another.  Strips past the last are computed and left.
+  const int i = wave & (fm - 1), j0 = wave >> fms, js = kSmallWaves >> fms;      // fragment f is (i, j0 + js f)
+  auto square = [&](const uint8_t* x, int pitch, int k16, auto done) {
+    if (j0 >= fm) return;
+    v16f d = zero;
+#pragma unroll 4
+    for (int s = 0; s < k16; ++s)
+      d = __builtin_amdgcn_mfma_f32_32x32x16_f16(strip_of(x, pitch, j0, s), rows_of(x, pitch, i, s), d, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float o[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) o[r] = d[8 * q + r];
+      done(32 * i + l32, 32 * j0 + 16 * q + 8 * h, o);
+    }
+  };
+  auto squares = [&](bool last) {
+    // A = X X^T
+    square(sX, px, v.n / 16, [&](int m, int n, const float (&o)[8]) {
+      v8h y;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) y[r] = (half_t)(o[r] * (kScaleA / (kScaleX * kScaleX)));
+      *(v8h*)(sA + m * ps + 2 * n) = y;
+    });
+    __syncthreads();
+    // B = b A + c A A, and a on its diagonal in the last step
+    const float fb = (float)(step.b / kScaleA), fc = (float)(step.c / ((double)kScaleA * kScaleA));
+    const float fa = last ? (float)step.a : 0.0f;
+    square(sA, ps, v.m / 16, [&](int m, int n, const float (&o)[8]) {
+      const v8h base = *(const v8h*)(sA + m * ps + 2 * n);
+      v8h y;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        float b = fmaf(fb, (float)base[r], o[r] * fc);
+        if (n + r == m) b += fa;
+        y[r] = (half_t)b;
+      }
+      *(v8h*)(sB + m * ps + 2 * n) = y;
+    });
+    __syncthreads();
+  };
+  v16f d[NF];
+  auto products_of_x = [&]() {
+#pragma unroll
+    for (int f = 0; f < NF; ++f) d[f] = zero;
+#pragma unroll 2
+    for (int s = 0; s < v.m / 16; ++s) {
+      const v8h p = rows_of(sB, ps, i, s);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const int j = j0 + js * f < v.n / 32 ? j0 + js * f : 0;
+        d[f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(columns_of(sX, px, j, s), p, d[f], 0, 0, 0);
+      }
+    }
+  };
+#pragma unroll 1
+  for (int k = 0; k < step.steps; ++k) {
+    keep_x();
+    squares(k + 1 == step.steps);
+    products_of_x();
+    // X' = a X + B X
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = fmaf((float)step.a, (float)low[f][q][e] + (float)high[f][q][e], d[f][8 * q + e]);
+          high[f][q][e] = (half_t)y;
+          low[f][q][e] = (half_t)(y - (float)high[f][q][e]);
+        }
+    }
+  }
+  // the last step's B X is the result
+  __syncthreads();
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    int i, j;
+    if (!strips(f, i, j)) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      whole[(32 * i + l32) * pw + 32 * j + 16 * (r / 8) + 8 * h + r % 8] = d[f][r] * (1.0f / kScaleX);
+  }
+  __syncthreads();
+  float keep, rate;
+  rates(t, step, keep, rate);
+  {
+#pragma clang fp contract(off)
+    float w[kAtOnce][4];
+    batches(
+        [&](int e, int row, int col) {
+          const int count = count_of(row, col);
+          if (t.w != nullptr && count > 0) load_values(t.w + row * t.cols + col, count, w[e]);
+        },
+        [&](int e, int row, int col) {
+          const int count = count_of(row, col);
+          if (count <= 0) return;
+          float o[4];
+          if (tall) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = k < count ? whole[(col + k) * pw + row] : 0.0f;
+          } else {
+            const v4f y = *(const v4f*)(whole + row * pw + col);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = y[k];
+          }
+          const int at = row * t.cols + col;
+          const int64_t to = row * t.ld_out + col;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= count) continue;
+            if (t.w != nullptr) {
+              const float x = w[e][k] * keep - o[k] * rate;
+              t.w[at + k] = x;
+              if (t.copy != nullptr) t.copy[at + k] = (uint16_t)pack_bf16(x, 0.0f);
+            } else if (t.out_bf16) {
+              ((uint16_t*)t.out)[to + k] = (uint16_t)pack_bf16(o[k], 0.0f);
+            } else {
+              ((float*)t.out)[to + k] = o[k];
+            }
+          }
+        });
+  }
+}
+
+// Whether every item fits ortho_small; launches it if so.
+bool small_items(const Args& a, const OrthoStep& step, hipStream_t s) {
+  int64_t bytes = 0;
+  for (int i = 0; i < a.count; ++i) {
+    const OrthoSize z = ortho_size(a.item[i].rows, a.item[i].cols);
+    if (!ortho_small_fits(z)) return false;
+    const int64_t need = ortho_small_bytes(z);
+    bytes = need > bytes ? need : bytes;
+  }
+  const dim3 g((unsigned)a.count), b(kSmallThreads);
+  hipLaunchKernelGGL(ortho_small, g, b, (uint32_t)bytes, s, a, step);
+  return true;
+}
+
 // a's items by falling `key`, so that the longest tiles start first.
 template <typename Key>
 void sort_items(Args& a, const Key& key) {
@@ -788,6 +1086,7 @@ hipError_t launch_ortho(const OrthoItem* items, int count, const OrthoStep& step
   Args a;
   a.count = count;
   for (int i = 0; i < kOrthoGroup; ++i) a.item[i] = items[i < count ? i : count - 1];
+  if (small_items(a, step, s)) return hipGetLastError();
   int total = deal(a, [](const OrthoItem& t) { return (int)ortho_size(t.rows, t.cols).parts; });
   hipLaunchKernelGGL(ortho_sum, dim3((unsigned)total), dim3(kSumThreads), 0, s, a, step);
   total = deal(a, [](const OrthoItem& t) {

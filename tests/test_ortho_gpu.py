@@ -79,6 +79,20 @@ def test_lists(shapes):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+SMALL = [(128, 256), (256, 128), (64, 512), (512, 64), (100, 250), (500, 17), (1, 512), (512, 1), (1, 513), (128, 192), (5, 3)]
+
+
+@pytest.mark.parametrize("shapes", [[s] for s in SMALL] + [SMALL, SMALL * 4, SMALL + [(129, 64)], [(64, 64), (500, 300)]])
+def test_small_matrices(shapes):
+    """Matrices that one workgroup takes whole, alone, together, more than a launch's, and beside one that is larger."""
+    announce("ortho small %s" % shapes[:3])
+    pairs = [gradient(*s, 20 + i, torch.bfloat16 if i % 2 else torch.float32) for i, s in enumerate(shapes)]
+    got = orthogonalize([g for g, _ in pairs], out_dtype=torch.float32)
+    for o, (g, v), shape in zip(got, pairs, shapes):
+        check(o, v, shape)
+    assert all(torch.equal(a, b) for a, b in zip(got, orthogonalize([g for g, _ in pairs], out_dtype=torch.float32)))
+
+
 def test_large_against_float64_on_the_gpu():
     """A square matrix of a large layer, and a wide one: every tile and a whole round of the chip."""
     for rows, cols in ((4096, 4096), (2048, 7936), (6016, 1920)):
@@ -186,8 +200,12 @@ def tensors_of(shapes, seed, dtype=torch.float32, copies=True):
 @pytest.mark.parametrize("adjust", ["rms", "shape", "plain"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_muon_step(dtype, adjust, nesterov):
-    shapes = [(200, 130), (64, 300), (65, 65), (1, 9), (300, 2)]
-    announce("muon %s %s %s" % (dtype, adjust, nesterov))
+    for shapes in ([(200, 130), (64, 300), (65, 65), (1, 9), (300, 2)], [(128, 256), (200, 70), (65, 65), (1, 9), (300, 2)]):
+        announce("muon %s %s %s %s" % (dtype, adjust, nesterov, shapes))
+        one_step(shapes, dtype, adjust, nesterov)
+
+
+def one_step(shapes, dtype, adjust, nesterov):
     t = tensors_of(shapes, 7, dtype, copies=adjust != "plain")
     before = [[x.double().cpu().numpy() for x in t[k]] for k in "wgm"]
     scale = torch.tensor([0.5], device="cuda") if adjust == "shape" else None

@@ -433,15 +433,13 @@ struct Coef {
   int left, right, add, add2, out;       // squares
 };
 
+// t: the workgroup's matrix, id: its number in it, lds: room for S stages of both operands
 template <int F, int S, int MODE, bool TRANS>
-__global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a, const OrthoStep step, const Coef c) {
+__device__ __forceinline__ void product_tile(const OrthoItem t, int id, const OrthoStep& step, const Coef& c,
+                                             uint8_t* lds) {
   constexpr bool kSym = MODE <= kMix;
   constexpr int T = 64 * F, kStage = T * kRow;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S * kStage];      // the first operand's stages, the second's
-  uint8_t *const sP = lds, *const sQ = lds + S * kStage;
-  int id;
-  const OrthoItem t = a.item[find(a, id)];
-  if (!kSym && MODE == kLast && (t.rows > t.cols) != TRANS) return;
+  uint8_t *const sP = lds, *const sQ = lds + S * kStage;               // the first operand's stages, the second's
   const View v = view(t);
   // An XCD (workgroup ids are dealt to them in turn, items start at a multiple of 8) takes a contiguous run of tiles.
   const int tm = (v.m + T - 1) / T, tn = kSym ? tm : (v.n + T - 1) / T, tiles = kSym ? tm * (tm + 1) / 2 : tm * tn;
@@ -1035,6 +1033,21 @@ void sort_items(Args& a, const Key& key) {
     for (int k = i; k > 0 && key(a.item[k - 1]) < key(a.item[k]); --k) std::swap(a.item[k - 1], a.item[k]);
 }
 
+// (The item by value: by reference, the tall matrices' last step spilled its accumulators.)
+template <int F, int S, int MODE>
+__global__ void __launch_bounds__(256, F < 3 ? 2 : 1) ortho_product(const Args a, const OrthoStep step, const Coef c) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S * 64 * F * kRow];
+  int id;
+  const OrthoItem t = a.item[find(a, id)];
+  if constexpr (MODE == kLast) {
+    if (t.rows > t.cols) {
+      product_tile<F, S, MODE, true>(t, id, step, c, lds);
+      return;
+    }
+  }
+  product_tile<F, S, MODE, false>(t, id, step, c, lds);
+}
+
 // Workgroups of each item, `of(item)` of them, as a's table; their number.
 template <typename Of>
 int deal(Args& a, const Of& of) {
@@ -1052,13 +1065,7 @@ void products(Args& a, const OrthoStep& step, const Coef& c, hipStream_t s) {
     const OrthoSize z = ortho_size(t.rows, t.cols);
     return (int)((ortho_tiles(z, MODE <= kMix, F) + kXcds - 1) / kXcds * kXcds);
   });
-  bool wide = MODE != kLast, tall = false;
-  if (MODE == kLast)
-    for (int i = 0; i < a.count; ++i) (a.item[i].rows > a.item[i].cols ? tall : wide) = true;
-  if (wide) hipLaunchKernelGGL((ortho_product<F, S, MODE, false>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
-  if constexpr (MODE == kLast) {
-    if (tall) hipLaunchKernelGGL((ortho_product<F, S, MODE, true>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
-  }
+  hipLaunchKernelGGL((ortho_product<F, S, MODE>), dim3((unsigned)total), dim3(256), 0, s, a, step, c);
 }
 
 // The tile whose time for these items is the least.

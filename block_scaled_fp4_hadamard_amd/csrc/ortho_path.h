@@ -69,18 +69,20 @@ inline void each_ortho_group(const T* list, int32_t count, const Visit& visit) {
 // three LDS stages or two with two.
 enum class OrthoTile { k64, k128, k128Two, k192, k256 };
 
-// What a tile costs (us): `start` for its first copies and its epilogue, and a step of 64 k, `alone` where few CUs work
-// and `shared` for a CU's part of a full chip, which power slows.  Fitted to 64 x 64 .. 4096 x 14336.
+// What a tile costs (us): `sym` or `full` for its first copies and its epilogue (of a square, of X), and a step of 64 k,
+// `alone` where few CUs work and `shared` for a CU's part of a full chip, which power slows.  Fitted to 64 x 64 .. 4096 x
+// 14336.  For example 4096 x 4096 (A / X): tiles of 64 163 / 223 us, of 128 105 / 158 and (two) 100 / 146, of 192 71 / 146,
+// of 256 90 / 125; 1024 x 1024: 7.5 / 8.7, 11 / 13, 13 / 15, 17 / 22, 26 / 34.
 struct OrthoCost {
   OrthoTile tile;
   int f, per;                                      // the tile's side in 64s, workgroups of a CU
-  double start, alone, shared;
+  double sym, full, alone, shared;
 };
-constexpr OrthoCost kOrthoCosts[] = {{OrthoTile::k64, 1, 2, 4.0, 0.17, 0.25},
-                                     {OrthoTile::k128, 2, 1, 6.0, 0.30, 0.58},
-                                     {OrthoTile::k128Two, 2, 2, 6.0, 0.36, 0.56},
-                                     {OrthoTile::k192, 3, 1, 8.0, 0.52, 0.95},
-                                     {OrthoTile::k256, 4, 1, 14.0, 0.87, 1.55}};
+constexpr OrthoCost kOrthoCosts[] = {{OrthoTile::k64, 1, 2, 3.0, 4.0, 0.17, 0.22},
+                                     {OrthoTile::k128, 2, 1, 6.0, 8.5, 0.30, 0.58},
+                                     {OrthoTile::k128Two, 2, 2, 6.0, 8.5, 0.36, 0.56},
+                                     {OrthoTile::k192, 3, 1, 8.0, 14.0, 0.52, 0.95},
+                                     {OrthoTile::k256, 4, 1, 12.0, 24.0, 0.87, 1.55}};
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
 
@@ -102,13 +104,14 @@ inline double ortho_time(const OrthoSize* sizes, int count, bool sym, bool gram,
   const double longest = (double)((gram ? sizes[0].n : sizes[0].m) / 64);
   const double shortest = (double)((gram ? sizes[count - 1].n : sizes[count - 1].m) / 64);
   const double slots = (double)(kCus * c.per), rounds = floor(tiles / slots), rest = tiles - rounds * slots;
-  double us = rounds * c.start;
+  const double start = sym ? c.sym : c.full;
+  double us = rounds * start;
   if (rounds > 0.0) us += (steps - rest * shortest) / kCus * c.shared;
   if (rest > 0.0) {
     const double k = rounds > 0.0 ? shortest : steps / tiles;
-    us += c.start + k * (c.alone + (c.per * c.shared - c.alone) * rest / slots);
+    us += start + k * (c.alone + (c.per * c.shared - c.alone) * rest / slots);
   }
-  const double least = c.start + longest * c.alone;
+  const double least = start + longest * c.alone;
   return us > least ? us : least;
 }
 

@@ -132,8 +132,7 @@ inline OrthoTile ortho_choose(const OrthoSize* sizes, int count, bool sym, bool 
 // sixteen rows' 16-byte pieces, and four rows' 64-byte ones (almost), lie in different banks.
 inline __attribute__((always_inline)) constexpr int ortho_pitch(int n) { return 2 * n + (2 * n % 256 == 0 ? 80 : 208); }
 
-// Matrices that one workgroup takes whole: X, A and B in LDS.  128 x 256 take 20 us instead of 70, 64 x 64 13 instead
-// of 55.
+// Matrices that one workgroup takes whole: X, A and B in LDS (128 x 256: 43 us instead of 66).
 inline int64_t ortho_small_bytes(const OrthoSize& z) {
   const int64_t products = z.m * ortho_pitch((int)z.n) + 2 * z.m * ortho_pitch((int)z.m), whole = 4 * z.m * (z.n + 4);
   return products > whole ? products : whole;
@@ -141,8 +140,8 @@ inline int64_t ortho_small_bytes(const OrthoSize& z) {
 inline bool ortho_small_fits(const OrthoSize& z) { return z.m <= 128 && z.m * z.n <= 32768; }
 
 // Whether the first two steps of these matrices run as one: it replaces 3 m^2 n multiplications by 3 m^3 (symmetric
-// products counted half) and saves a pass of X, for one launch more, which large products do not notice.  4096 x 14336:
-// 4.27 ms against 4.83; 4096 x 4096: 1.36 against 1.34.
+// products counted half) and saves a pass of X, for one launch more, which large products do not notice.  A block's four
+// linears: 13.87 ms against 15.45; 4096 x 4096 alone: 1.58 either way.
 template <typename T>
 inline bool ortho_joins(const T* list, int count) {
   double wide = 0.0, square = 0.0;

@@ -561,10 +561,10 @@ int64_t mx_layer_norm_grad_workspace(int64_t rows, int64_t cols, mx_out type, in
  * turn each singular value s of X into a s + b s^3 + c s^5, step by step, and
  * leave its singular vectors: with a = 3.4445, b = -4.7750, c = 2.0315 and five
  * steps all but the weakest end between 0.68 and 1.13.
- * The products take float16 operands (X times 2^12, A and B times 2^11) and sum
- * in float32; X is carried from step to step as two float16 parts, 22 bits.  The
- * result is off by up to about 2e-3 of its norm before it is rounded.  A matrix
- * that holds Inf or NaN becomes NaN; one of zeros stays zero.
+ * The products take float16 operands and sum in float32; X is carried from step
+ * to step as two float16 parts, 22 bits.  With these coefficients the result is
+ * off by up to about 2e-3 of its norm before it is rounded.  A matrix that holds
+ * Inf or NaN becomes NaN; one of zeros stays zero.
  */
 typedef struct {
   double a, b, c;     /* such that X and its factors stay small from singular

@@ -240,3 +240,40 @@ def test_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         eager = both()
         assert all(torch.equal(p, q) for p, q in zip(got, eager))
+
+
+def test_two_calls_at_once():
+    """Two streams at once, each call with its own workspace."""
+    announce("norm two at once")
+    sets = [case(700, cols, torch.bfloat16, 14 + k) for k, cols in enumerate((4096, 17000))]
+    want = [layer_norm_grad(s[2], s[0], *layer_norm(s[0])[1:]) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for s, stream in zip(sets, streams):
+        with torch.cuda.stream(stream):
+            got.append([layer_norm_grad(s[2], s[0], *layer_norm(s[0])[1:]) for _ in range(4)][-1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(1, 1, torch.float32), (300, 4096, torch.bfloat16), (5, 14000, torch.float32),
+                                             (260, 19456, torch.bfloat16), (3, 19457, torch.float32)])
+def test_workspace_is_all_that_is_written(rows, cols, dtype):
+    """The C entry with a workspace of exactly its size between guards."""
+    from block_scaled_fp4_hadamard_amd import _lib
+    announce("norm workspace %d x %d" % (rows, cols))
+    lib = _lib.lib()
+    x, _, dy, _ = case(rows, cols, dtype, 16)
+    _, mean, rstd = layer_norm(x)
+    kind = 0 if dtype == torch.float32 else 1
+    size = lib.mx_layer_norm_grad_workspace(rows, cols, kind, 1)
+    buf = torch.full((size + 8192,), 255, dtype=torch.uint8, device="cuda")
+    dx, dw, db = torch.empty_like(x), torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    torch.cuda.synchronize()
+    st = lib.mx_layer_norm_grad(dy.data_ptr(), cols, x.data_ptr(), cols, kind, rows, cols, None, 0, mean.data_ptr(),
+                                rstd.data_ptr(), 0, dx.data_ptr(), cols, dw.data_ptr(), db.data_ptr(),
+                                buf.data_ptr() + 4096, size, None)
+    torch.cuda.synchronize()
+    assert st == 0 and bool((buf[:4096] == 255).all()) and bool((buf[4096 + size:] == 255).all())
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), layer_norm_grad(dy, x, mean, rstd)))

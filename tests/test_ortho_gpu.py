@@ -182,6 +182,61 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(got, orthogonalize(gs)))
 
 
+def test_two_calls_at_once():
+    """Two streams, and two captured graphs replayed on them, each with its own workspace: small, middle and large."""
+    announce("ortho two at once")
+    sets = [[gradient(*s, 30 + k)[0] for s in ((300, 500), (1024, 900))] + [gradient(128, 256, 40 + k)[0]]
+            for k in range(2)]
+    want = [[orthogonalize(g) for g in gs] for gs in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for k in range(2):
+        with torch.cuda.stream(streams[k]):
+            got[k] = [orthogonalize(g) for _ in range(3) for g in sets[k]][-3:]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+    graphs, outs = [], []
+    for k in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append([orthogonalize(g) for g in sets[k]])
+        graphs.append(graph)
+    for _ in range(3):
+        for o in outs[0] + outs[1]:
+            o.fill_(0.0)
+        torch.cuda.synchronize()
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(outs, want) for a, b in zip(x, y))
+
+
+def test_workspace_is_all_that_is_written():
+    """The C entry with a workspace of exactly its size between guards, at sizes of every tile; twice on a workspace that
+    holds NaN, so that nothing it held before comes through."""
+    from block_scaled_fp4_hadamard_amd import _lib
+    announce("ortho workspace")
+    lib = _lib.lib()
+    for shapes in ([(128, 256)], [(300, 180)], [(2048, 1990)], [(1000, 2900), (2900, 1000)], [(4096, 4160)]):
+        gs = [gradient(*s, 50, torch.bfloat16)[0] if s[0] < 4000 else torch.randn(s, device="cuda").bfloat16()
+              for s in shapes]
+        outs = [torch.empty_like(g) for g in gs]
+        array = (_lib.OrthoMatrixC * len(gs))(*[
+            _lib.OrthoMatrixC(g.data_ptr(), o.data_ptr(), *g.shape, g.shape[1], g.shape[1], 1, 1)
+            for g, o in zip(gs, outs)])
+        size = lib.mx_orthogonalize_workspace(array, len(gs))
+        buf = torch.full((size + 8192,), 255, dtype=torch.uint8, device="cuda")        # float16 NaN everywhere
+        args = (array, len(gs), _lib.OrthoParamsC(3.4445, -4.7750, 2.0315, 1e-7, 5), buf.data_ptr() + 4096, size, None)
+        torch.cuda.synchronize()
+        assert lib.mx_orthogonalize(*args) == 0
+        torch.cuda.synchronize()
+        assert bool((buf[:4096] == 255).all()) and bool((buf[4096 + size:] == 255).all())
+        assert all(torch.equal(o, w) for o, w in zip(outs, orthogonalize(gs)))
+        del buf
+
+
 # ---- the Muon step
 
 

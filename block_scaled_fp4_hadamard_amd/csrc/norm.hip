@@ -597,13 +597,15 @@ struct Shape {
   int threads;                   // of a workgroup
 };
 
-// The lanes of a row, for `cols` elements of e a vector.
+// The lanes of a row, for `cols` elements of e a vector.  A wave for 129 to 192 vectors, which leave half of 256 lanes idle
+// (59898 x 516 float32: 42 us forward and 78 backward for 61 and 112).
 Shape forward_shape(int64_t cols, int e) {
   const int64_t v = (cols + e - 1) / e;
   if (v <= 16) return {16, 1, 256};
   if (v <= 32) return {16, 2, 256};
   if (v <= 64) return {64, 1, 256};
   if (v <= 128) return {64, 2, 256};
+  if (v <= 192) return {64, 3, 256};
   if (v <= 256) return {256, 1, 256};
   if (v <= 512) return {256, 2, 256};
   if (v <= 1024) return {256, 4, 256};
@@ -620,6 +622,7 @@ Shape grad_shape(int64_t cols, int64_t rows, int e) {
   Shape s = {0, 0, 1024};
   if (v <= 32) s = {16, v <= 16 ? 1 : 2, 1024};
   else if (v <= 128) s = {64, v <= 64 ? 1 : 2, 1024};
+  else if (v <= 192 && e == 4) s = {64, 3, 1024};       // bf16: its 24 columns a lane leave too few registers
   else if (v <= 512) s = {256, v <= 256 ? 1 : 2, 1024};
   else if (v <= 1024) return {1024, 1, 1024};
   else if (v <= 2048 && e == 4) return {1024, 2, 1024};
@@ -648,7 +651,7 @@ hipError_t forward(const NormParams& p, bool wbf, hipStream_t st) {
     hipLaunchKernelGGL((norm_kernel<T, KIND, LANES, VECTORS>), g, dim3(LANES < 256 ? 256 : LANES), 0, st, p, wbf); \
     return hipGetLastError();                                                                                   \
   }
-  MX_NORM_CASE(16, 1) MX_NORM_CASE(16, 2) MX_NORM_CASE(64, 1) MX_NORM_CASE(64, 2) MX_NORM_CASE(256, 1)
+  MX_NORM_CASE(16, 1) MX_NORM_CASE(16, 2) MX_NORM_CASE(64, 1) MX_NORM_CASE(64, 2) MX_NORM_CASE(64, 3) MX_NORM_CASE(256, 1)
   MX_NORM_CASE(256, 2) MX_NORM_CASE(256, 4) MX_NORM_CASE(256, 6) MX_NORM_CASE(256, 8) MX_NORM_CASE(1024, 4)
 #undef MX_NORM_CASE
   hipLaunchKernelGGL((norm_wide<T, KIND>), g, dim3(1024), 0, st, p, wbf);
@@ -670,7 +673,7 @@ hipError_t backward(const NormGradParams& p, bool wbf, float* ws, hipStream_t st
   MX_NORM_CASE(64, 1, 1024) MX_NORM_CASE(64, 2, 1024) MX_NORM_CASE(256, 1, 1024) MX_NORM_CASE(256, 2, 1024)
   MX_NORM_CASE(1024, 1, 1024)
   if constexpr (sizeof(T) == 4) {
-    MX_NORM_CASE(1024, 2, 1024)
+    MX_NORM_CASE(64, 3, 256) MX_NORM_CASE(64, 3, 1024) MX_NORM_CASE(1024, 2, 1024)
   }
 #undef MX_NORM_CASE
 #define MX_NORM_CASE(VECTORS)                                                                                      \

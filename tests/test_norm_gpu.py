@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24            # half a float32 step, relative
 HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
 # every layout of a row (16, 64, 256 and 1024 lanes, one to four vectors), its borders, and rows wider than a workgroup
-WIDTHS = [1, 3, 8, 64, 127, 128, 129, 256, 257, 512, 1000, 1025, 2048, 4096, 4099, 8192, 8200, 16384, 16385, 33000]
+WIDTHS = [1, 3, 8, 64, 127, 128, 129, 256, 257, 512, 516, 768, 1000, 1100, 1536, 1025, 2048, 4096, 4099, 8192, 8200, 16384, 16385, 33000]
 
 
 def depth(cols):
@@ -116,7 +116,7 @@ def test_rows_of_every_width(cols, dtype, kind):
         check_backward(dy, vdy, x, vx, w, kind, got[1], got[2], back)
 
 
-@pytest.mark.parametrize("rows,cols", [(5000, 64), (20001, 128), (3000, 512), (4097, 1024), (2001, 4096), (1500, 9001)])
+@pytest.mark.parametrize("rows,cols", [(5000, 64), (20001, 128), (3000, 512), (3001, 600), (4097, 1024), (2001, 4096), (1500, 9001)])
 def test_many_rows(rows, cols):
     """More rows than the resident workgroups take at once, the last round part-filled."""
     announce("norm rows %d x %d" % (rows, cols))

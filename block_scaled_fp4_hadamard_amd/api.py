@@ -712,7 +712,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, kind="layer", out=None):
     and no bias: (y, mean, rstd), y in x's type, the rows' float32 statistics for layer_norm_grad (mean None for "rms").
 
     weight and bias: cols elements of one type, float32 or bfloat16 (None: ones, zeros).  out: y's place, apart from the
-    inputs.
+    inputs.  Rows without columns have statistics of NaN.
     """
     if kind not in _NORM:
         raise ValueError("unknown kind %r" % (kind,))
@@ -731,6 +731,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, kind="layer", out=None):
         _apart(out, (("x", x), ("weight", weight), ("bias", bias)))
     mean = x.new_empty(rows, dtype=torch.float32) if kind == "layer" else None
     rstd = x.new_empty(rows, dtype=torch.float32)
+    if rows and not cols:               # means of nothing, which the library leaves alone
+        for stat in (mean, rstd):
+            if stat is not None:
+                stat.fill_(float("nan"))
     _launch(at, "mx_layer_norm", _lib.lib().mx_layer_norm, x.data_ptr(), dtype, rows, cols, ld, w, b, wtype, eps,
             _NORM[kind], y.data_ptr(), ld_y, mean.data_ptr() if mean is not None else None, rstd.data_ptr())
     if out is not None:

@@ -514,7 +514,8 @@ typedef enum { MX_NORM_LAYER = 0, MX_NORM_RMS = 1 } mx_norm_kind;
  *   x, y       device, row-major, both of `type`, aligned to it; rows ld_x and
  *              ld_y elements apart, >= cols (16-byte aligned rows: fastest);
  *              y must not overlap x
- *   rows, cols either 0: nothing to do, MX_OK; rows < 2^40, cols < 2^30
+ *   rows, cols either 0: nothing to do, MX_OK (with cols 0 the statistics are
+ *              not written); rows < 2^40, cols < 2^30
  *   weight, bias  device, cols elements of `weight_type`; NULL: ones, zeros;
  *              bias is NULL for MX_NORM_RMS
  *   eps        finite, >= 0 (with 0 a constant row, or an RMS row of zeros,

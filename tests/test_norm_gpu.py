@@ -277,3 +277,15 @@ def test_workspace_is_all_that_is_written(rows, cols, dtype):
     torch.cuda.synchronize()
     assert st == 0 and bool((buf[:4096] == 255).all()) and bool((buf[4096 + size:] == 255).all())
     assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), layer_norm_grad(dy, x, mean, rstd)))
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_statistics_of_rows_without_columns(kind):
+    """0 / 0, and not what the memory held before."""
+    announce("norm stats of nothing %s" % kind)
+    held = [torch.full((5,), 7.0, device="cuda") for _ in range(16)]
+    del held
+    for dtype in (torch.float32, torch.bfloat16):
+        _, mean, rstd = layer_norm(torch.zeros((5, 0), dtype=dtype, device="cuda"), kind=kind)
+        assert rstd.shape == (5,) and rstd.isnan().all()
+        assert mean is None if kind == "rms" else mean.isnan().all()

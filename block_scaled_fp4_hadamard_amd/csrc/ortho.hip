@@ -181,12 +181,14 @@ __device__ __forceinline__ void load_gradient(const OrthoItem& t, int64_t at, fl
   o = (t.g_bf16 ? bf16_value(((const uint16_t*)t.g)[at]) : ((const float*)t.g)[at]) * scale;
 }
 
-// U's scale 2^12 / (|U| + eps), whose float32 might overflow or sink, in two factors
+// U's scale 2^12 / (|U| + eps), whose float32 might overflow or sink, in two factors; 0 for a matrix of zeros, where
+// that of the smallest eps would be Inf
 struct Scale {
   float factor;
   int power;
 };
 __device__ __forceinline__ Scale scale_of(double sum, double eps) {
+  if (sum == 0.0) return Scale{0.0f, 0};
   int power;
   const double f = frexp((double)kScaleX / (sqrt(sum) + eps), &power);
   return Scale{(float)f, power};

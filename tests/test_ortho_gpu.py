@@ -357,3 +357,15 @@ def test_a_layer_with_its_norm():
             # linear in the vector: differences are exact up to float64, the kernel up to float32's sums
             size = float((d64[:, at].abs() * (h[:, at].abs() if which == 0 else 1.0)).sum())
             assert abs((loss[0] - loss[1]) / 2e-3 - float(grad[at])) <= 300 * 2.0 ** -24 * size + 1e-9
+
+
+@pytest.mark.parametrize("shape", [(100, 64), (300, 200)])
+def test_zeros_stay_zeros_with_any_eps(shape):
+    """One workgroup's kernel and the tiles', down to the smallest double."""
+    announce("ortho zeros %s" % (shape,))
+    for eps in (1e-7, 1e-300, 1e-306, 5e-324):
+        assert not orthogonalize(torch.zeros(shape, device="cuda"), eps=eps, out_dtype=torch.float32).any()
+    w = torch.ones(shape, device="cuda")
+    z = torch.zeros_like(w)
+    muon_step(MuonTensors([w], [z], [z.clone()]), lr=0.5, weight_decay=0.0, eps=1e-306)
+    assert torch.equal(w, torch.ones_like(w))

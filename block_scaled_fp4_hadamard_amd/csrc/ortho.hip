@@ -193,7 +193,8 @@ __device__ __forceinline__ Scale scale_of(double sum, double eps) {
   const double f = frexp((double)kScaleX / (sqrt(sum) + eps), &power);
   return Scale{(float)f, power};
 }
-__device__ __forceinline__ float scaled(float u, const Scale& s) { return ldexpf(u * s.factor, s.power); }
+// the power first: it is exact, takes u to at most 2^13, and makes a subnormal u a normal number before the product rounds
+__device__ __forceinline__ float scaled(float u, const Scale& s) { return ldexpf(u, s.power) * s.factor; }
 
 constexpr int kSumThreads = 1024;
 

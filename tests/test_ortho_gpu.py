@@ -369,3 +369,16 @@ def test_zeros_stay_zeros_with_any_eps(shape):
     z = torch.zeros_like(w)
     muon_step(MuonTensors([w], [z], [z.clone()]), lr=0.5, weight_decay=0.0, eps=1e-306)
     assert torch.equal(w, torch.ones_like(w))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(64, 96), (300, 200), (200, 300)])
+def test_subnormal_gradients(shape, dtype):
+    """Whole multiples of the type's smallest number are as good a gradient as any."""
+    announce("ortho subnormal %s %s" % (shape, dtype))
+    rng = np.random.default_rng([60, *shape])
+    v = rng.integers(1, 64, shape) * np.sign(rng.standard_normal(shape)) * torch.finfo(dtype).smallest_normal * \
+        torch.finfo(dtype).eps
+    g = torch.from_numpy(v).to(dtype).cuda()
+    assert np.array_equal(g.double().cpu().numpy(), v)
+    check(orthogonalize(g, eps=1e-60, out_dtype=torch.float32), v, "subnormal %s" % (shape,), eps=1e-60)

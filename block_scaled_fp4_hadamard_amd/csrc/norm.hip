@@ -568,27 +568,32 @@ __global__ void __launch_bounds__(256) norm_grad_wide_cols(const NormGradParams 
   }
 }
 
-// dweight and dbias from the workgroups' sums: 64 columns a workgroup, its 16 waves a run of the sums each.
+// dweight and dbias from the workgroups' sums: 64 columns a workgroup at a time, its 16 waves a run of the sums each.
+constexpr int64_t kSumGrid = int64_t(1) << 21;    // workgroups of 1024 lanes: a launch holds less than 2^32 lanes
+
 __global__ void __launch_bounds__(1024) norm_grad_sum(const float* parts, int count, int64_t cols, float* dweight,
                                                       float* dbias) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t at = (int64_t)blockIdx.x * 64 + lane;
   float* out = blockIdx.y ? dbias : dweight;
   if (out == nullptr) return;
-  const float* x = parts + (int64_t)blockIdx.y * cols + at;
   const int run = (count + 15) / 16, to = min(count, (wave + 1) * run);
-  float s = 0.0f;
-  if (at < cols) {
+  for (int64_t base = (int64_t)blockIdx.x * 64; base < cols; base += (int64_t)gridDim.x * 64) {
+    const int64_t at = base + lane;
+    const float* x = parts + (int64_t)blockIdx.y * cols + at;
+    float s = 0.0f;
+    if (at < cols) {
 #pragma unroll 4
-    for (int i = wave * run; i < to; ++i) s += x[(int64_t)i * 2 * cols];
-  }
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && at < cols) {
+      for (int i = wave * run; i < to; ++i) s += x[(int64_t)i * 2 * cols];
+    }
+    if (base >= (int64_t)gridDim.x * 64) __syncthreads();        // the columns before have been added
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && at < cols) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += red[i][lane];
-    out[at] = s;
+      for (int i = 1; i < 16; ++i) s += red[i][lane];
+      out[at] = s;
+    }
   }
 }
 
@@ -694,9 +699,11 @@ hipError_t backward(const NormGradParams& p, bool wbf, float* ws, hipStream_t st
     hipLaunchKernelGGL((norm_grad_wide_cols<T, KIND>), dim3((unsigned)((p.cols + 255) / 256), (unsigned)count),
                        dim3(256), 0, st, p, wbf, c, run, parts);
   }
-  if (sums)
-    hipLaunchKernelGGL(norm_grad_sum, dim3((unsigned)((p.cols + 63) / 64), 2), dim3(1024), 0, st, parts, (int)count,
-                       p.cols, p.dweight, p.dbias);
+  if (sums) {
+    const int64_t need = (p.cols + 63) / 64;
+    hipLaunchKernelGGL(norm_grad_sum, dim3((unsigned)(need < kSumGrid ? need : kSumGrid), 2), dim3(1024), 0, st, parts,
+                       (int)count, p.cols, p.dweight, p.dbias);
+  }
   return hipGetLastError();
 }
 

@@ -289,3 +289,24 @@ def test_statistics_of_rows_without_columns(kind):
         _, mean, rstd = layer_norm(torch.zeros((5, 0), dtype=dtype, device="cuda"), kind=kind)
         assert rstd.shape == (5,) and rstd.isnan().all()
         assert mean is None if kind == "rms" else mean.isnan().all()
+
+
+def test_gradient_of_more_columns_than_a_launch_has_lanes():
+    """The sums of 2^28 columns and more.  Values of -1, 0 and 1 and statistics of 0 and 1: every sum is a whole number
+    below 2^24, exact in any order, and dx is off by the roundings of its own four operations."""
+    announce("norm grad of 2^28 columns")
+    rows, cols = 2, (1 << 28) + 70
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    x, dy = (torch.randint(-1, 2, (rows, cols), generator=gen, device="cuda", dtype=torch.int8).bfloat16() for _ in range(2))
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dx, dw, db = layer_norm_grad(dy, x, mean, rstd)
+    step = 1 << 25
+    runs = [slice(a, a + step) for a in range(0, cols, step)]
+    c1, c2 = (sum(f(r) for r in runs) / cols for f in (lambda r: dy[:, r].double().sum(dim=1),
+                                                       lambda r: (dy[:, r].double() * x[:, r].double()).sum(dim=1)))
+    for r in runs:
+        g, h = dy[:, r].double(), x[:, r].double()
+        assert torch.equal(dw[r].double(), (g * h).sum(dim=0)) and torch.equal(db[r].double(), g.sum(dim=0))
+        want = g - c1[:, None] - h * c2[:, None]
+        tol = 4 * U * (g.abs() + c1.abs()[:, None] + h.abs() * c2.abs()[:, None])
+        assert bool(((dx[:, r].double() - want).abs() <= tol + HALF[torch.bfloat16] * (want.abs() + tol)).all())

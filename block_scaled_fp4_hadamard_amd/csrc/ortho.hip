@@ -17,9 +17,12 @@
 // what it adds in weak directions grows by a in every step, to a share of the
 // result where U has few strong directions.  So X is held in two parts, high and
 // low, 22 bits together (to 2^-25 in the low part's own scale); the products read
-// the high part, and the sum a X takes both.  Against float64 the result is off by 0.9e-3 to 1.6e-3 of
-// its norm, below what rounding it to bf16 costs (1.7e-3); with the high part
-// alone a matrix of rank 1 was 15% off.
+// the high part, and the sum a X takes both.  Against float64 the result is off by 0.5e-3 to 2.6e-3 of
+// its norm where the entries' roundings are independent, as rounding it to bf16
+// costs 1.7e-3; with the high part alone a matrix of rank 1 was 15% off.  The
+// worst is a matrix of equal entries: all entries of a square round alike, which
+// is an error of up to 2^-11 of B, and B at s = 1 is four times as large as the
+// factor a + b s^2 + c s^4 that it is a part of: up to 1.5e-2 after five steps.
 //
 // A list's matrices go through each product together, up to 32 in one launch:
 // the sums of squares, X, then three products a step; small ones through a single
@@ -1157,8 +1160,9 @@ hipError_t launch_ortho(const OrthoItem* items, int count, const OrthoStep& step
   int k = 0, from = 0;
   // The first two steps in one, where the list's matrices are wide: with P0 = a I + B0 and P1 = a I + B1 their factors, X2
   // = P1 P0 X0, and A1 = P0 A0 P0 comes from squares instead of a second pass over X.  That trades 3 m^2 n products for 3
-  // m^3 and a pass of X; the roundings of A1's detour are no larger than those of X1 X1^T.  (Three steps in one lose
-  // weak directions: 4e-3 off on a matrix of rank 1.)
+  // m^3 and a pass of X.  Where roundings are independent it costs up to a fifth of the error (rank 1: 1.4e-3 -> 1.6e-3;
+  // noise: 1.5e-3 either way); P1 P0 - a^2 is ten times P1 P0, which doubles the error of a constant matrix (at most
+  // 1.5e-2 -> 2.5e-2).  (Three steps in one lose weak directions: 4e-3 off on a matrix of rank 1.)
   if (step.steps >= 3 && ortho_joins(by_m.item, count)) {
     gram_of_x(0);                                    // 0: A0
     poly_of(0, 1, 0.0);                              // 1: B0

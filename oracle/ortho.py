@@ -25,7 +25,8 @@ def _half(v, scale):
     return (v * scale).astype(np.float16).astype(np.float64) / scale
 
 
-def orthogonalize_model(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+def orthogonalize_model(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7, joined=False):
+    """joined: the first two steps as one (steps >= 3), as the kernels take them for lists of large, wide matrices."""
     a, b, c = coefficients
     x = np.asarray(g, np.float64)
     tall = x.shape[0] > x.shape[1]
@@ -33,7 +34,18 @@ def orthogonalize_model(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
     x = x / (np.sqrt((x * x).sum()) + eps)
     hi = _half(x, SX)
     low = _half(x - hi, SX)
-    for k in range(steps):
+    first = 0
+    if joined:
+        s = _half(hi @ hi.T, SA)
+        f0 = _half(b * s + c * (s @ s), 1.0)
+        p = _half(a * s + f0 @ s, SA)
+        s = _half(a * p + f0 @ p, SA)
+        f1 = _half(b * s + c * (s @ s), 1.0)
+        x = a * a * (hi + low) + _half(a * f0 + a * f1 + f1 @ f0, 1.0) @ hi
+        hi = _half(x, SX)
+        low = _half(x - hi, SX)
+        first = 2
+    for k in range(first, steps):
         s = _half(hi @ hi.T, SA)
         f = b * s + c * (s @ s)
         if k + 1 == steps:

@@ -199,3 +199,68 @@ def test_lists_that_are_refused():
 def test_structs_match_the_header():
     assert ctypes.sizeof(_lib.OrthoMatrixC) == 56 and ctypes.sizeof(_lib.OrthoParamsC) == 40
     assert ctypes.sizeof(_lib.MuonTensorC) == 56 and ctypes.sizeof(_lib.MuonParamsC) == 88
+
+
+# ---- the documented error, on the oracle's model of the kernels' roundings
+
+
+def model_error(g, **kw):
+    ref = ortho.orthogonalize_ref(g, kw.get("steps", 5), kw.get("coefficients", ortho.COEFFICIENTS))
+    return np.linalg.norm(ortho.orthogonalize_model(g, **kw) - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("joined", [False, True])
+def test_error_of_independent_roundings(joined):
+    rng = np.random.default_rng(3)
+    for m, n in ((64, 64), (96, 300), (130, 700)):
+        low = rng.standard_normal((m, 4)) @ rng.standard_normal((4, n))
+        for g in (rng.standard_normal((m, n)), rng.standard_t(2, (m, n)), weight_gradient(rng, m, n, 16), low,
+                  rng.standard_normal((m, 1)) @ rng.standard_normal((1, n))):
+            assert model_error(g, joined=joined) <= 2.6e-3
+            assert model_error(g, joined=joined, steps=8) <= 4.5e-3
+            assert model_error(g, joined=joined, coefficients=(2.0, -1.5, 0.5)) <= 1e-3
+        assert model_error(low, joined=joined, steps=10) <= 5e-2
+
+
+@pytest.mark.parametrize("joined", [False, True])
+def test_error_of_roundings_that_are_alike(joined):
+    """Constant matrices, in the model's own arithmetic on their one singular value: an entry e of a square of side m is
+    the singular value m e.  The worst of many sizes stays within what is documented, and is no empty bound."""
+    a, b, c = ortho.COEFFICIENTS
+    half, sx, sa = ortho._half, ortho.SX, ortho.SA
+    rng = np.random.default_rng(4)
+    m = np.exp(rng.uniform(0, np.log(20000), 20000)).astype(int).astype(float)
+    n = np.floor(m * np.exp(rng.uniform(0, 5, m.size)))
+
+    def run(m, n):
+        x = 1.0 / np.sqrt(m * n)
+        hi = half(x, sx)
+        low = half(x - hi, sx)
+        if joined:
+            s = half(hi * hi * n, sa)
+            f0 = half(b * s + c * s * s * m, 1.0)
+            p = half(a * s + f0 * s * m, sa)
+            s = half(a * p + f0 * p * m, sa)
+            f1 = half(b * s + c * s * s * m, 1.0)
+            x = a * a * (hi + low) + half(a * f0 + a * f1 + f1 * f0 * m, 1.0) * m * hi
+            hi = half(x, sx)
+            low = half(x - hi, sx)
+        for k in range(2 if joined else 0, 5):
+            s = half(hi * hi * n, sa)
+            f = b * s + c * s * s * m
+            if k == 4:
+                return (half(f, 1.0) * (m - 1) + half(f + a, 1.0)) * hi
+            x = a * (hi + low) + half(f, 1.0) * m * hi
+            hi = half(x, sx)
+            low = half(x - hi, sx)
+
+    # the short form is the model
+    for p, q in ((40, 100), (85, 271)):
+        whole = ortho.orthogonalize_model(np.ones((p, q)), eps=0.0, joined=joined)
+        assert np.allclose(whole, run(float(p), float(q)), rtol=1e-12, atol=0)
+    s = 1.0
+    for _ in range(5):
+        s = a * s + b * s ** 3 + c * s ** 5
+    off = np.abs(run(m, n) * np.sqrt(m * n) / s - 1)
+    most = 2.5e-2 if joined else 1.5e-2
+    assert 0.6 * most < off.max() <= most

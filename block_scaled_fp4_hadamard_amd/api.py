@@ -804,15 +804,17 @@ def orthogonalize(g, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out_dtype=to
     """
     single = isinstance(g, torch.Tensor)
     gs = [g] if single else list(g)
-    if not gs:
-        return []
-    at = gs[0].get_device()
     if out is None:
         outs = [x.new_empty(x.shape, dtype=out_dtype) for x in gs]
     else:
         outs = [out] if single else list(out)
         if len(outs) != len(gs):
             raise ValueError("%d outputs for %d matrices" % (len(outs), len(gs)))
+    params, lib = _ortho_params(steps, coefficients, eps), _lib.lib()
+    if not gs:
+        _lib.check(lib.mx_orthogonalize(None, 0, params, None, 0, None), "mx_orthogonalize")   # only the checks
+        return []
+    at = gs[0].get_device()
     array = (_lib.OrthoMatrixC * len(gs))()
     for i, (x, o, c) in enumerate(zip(gs, outs, array)):
         name = "matrix %d" % i
@@ -825,12 +827,10 @@ def orthogonalize(g, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out_dtype=to
     if out is not None:
         for i, o in enumerate(outs):
             _apart(o, [("matrix %d" % j, x) for j, x in enumerate(gs)] + [("out %d" % j, x) for j, x in enumerate(outs[:i])])
-    lib = _lib.lib()
     # the workspace is this call's own: held until the launches, its memory then goes to later work of this stream only
     size = lib.mx_orthogonalize_workspace(array, len(gs))
     space = gs[0].new_empty(size, dtype=torch.uint8) if size else None
-    _launch(at, "mx_orthogonalize", lib.mx_orthogonalize, array, len(gs), _ortho_params(steps, coefficients, eps),
-            space.data_ptr() if size else None, size)
+    _launch(at, "mx_orthogonalize", lib.mx_orthogonalize, array, len(gs), params, space.data_ptr() if size else None, size)
     if out is not None:
         _written(outs)
     return outs[0] if single else outs

@@ -264,3 +264,12 @@ def test_error_of_roundings_that_are_alike(joined):
     off = np.abs(run(m, n) * np.sqrt(m * n) / s - 1)
     most = 2.5e-2 if joined else 1.5e-2
     assert 0.6 * most < off.max() <= most
+
+
+def test_a_list_of_no_matrices_is_checked_as_any():
+    assert orthogonalize([], out=[]) == []
+    with pytest.raises(ValueError, match="1 outputs for 0 matrices"):
+        orthogonalize([], out=[torch.zeros(8, 16)])
+    for kw in (dict(steps=0), dict(eps=0.0), dict(coefficients=(5.0, 0.0, 0.0))):
+        with pytest.raises(_lib.MXError):
+            orthogonalize([], **kw)

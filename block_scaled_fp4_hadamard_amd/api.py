@@ -796,7 +796,7 @@ def orthogonalize(g, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out_dtype=to
     coefficients (a, b, c), on X = g / (|g| + eps).
 
     A list's matrices, all on one device, are worked on together, which fills the chip where each alone does not.  The
-    products take float16 operands: after five steps of these coefficients the result is off by 0.5e-3 to 2.6e-3 of its
+    products take float16 operands: after five steps of these coefficients the result is off by 0.3e-3 to 2.6e-3 of its
     norm before it is rounded to out_dtype (float32 or bfloat16), and by up to 2.5e-2 where the entries or the singular
     values of g are all of one size.  More steps add to that; from ten on a matrix of low rank shows the noise of the
     directions that it does not have.  out: the result's place (a list for a list), apart from every g and from one

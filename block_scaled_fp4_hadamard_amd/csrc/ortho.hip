@@ -17,7 +17,7 @@
 // what it adds in weak directions grows by a in every step, to a share of the
 // result where U has few strong directions.  So X is held in two parts, high and
 // low, 22 bits together (to 2^-25 in the low part's own scale); the products read
-// the high part, and the sum a X takes both.  Against float64 the result is off by 0.5e-3 to 2.6e-3 of
+// the high part, and the sum a X takes both.  Against float64 the result is off by 0.3e-3 to 2.6e-3 of
 // its norm where the entries' roundings are independent, as rounding it to bf16
 // costs 1.7e-3; with the high part alone a matrix of rank 1 was 15% off.  The
 // worst is a matrix of equal entries: all entries of a square round alike, which

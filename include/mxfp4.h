@@ -565,15 +565,15 @@ int64_t mx_layer_norm_grad_workspace(int64_t rows, int64_t cols, mx_out type, in
  * The products take float16 operands and sum in float32; X is carried from step
  * to step as two float16 parts, 22 bits.  How far the result is off, in norm,
  * before it is rounded to its type, with these coefficients and five steps:
- *   0.5e-3 to 2.6e-3  noise, low rank, gradients of weights: the entries'
+ *   0.3e-3 to 2.6e-3  noise, low rank, gradients of weights: the entries'
  *                     roundings are independent of one another
  *   up to 1.5e-2      entries (or singular values) all of one size, at worst a
  *                     constant matrix: their roundings are alike and add up
  *   up to 2.5e-2      the same, where the first two steps run as one (large
  *                     matrices of which enough are wide)
- * Further steps add to it: eight leave 1e-3 to 4.5e-3 of the first kind, and a
+ * Further steps add to it: eight leave 1e-3 to 6e-3 of the first kind, and a
  * direction that G does not have grows by a factor a each step, in any
- * arithmetic: a matrix of low rank is about 1e-2 to 5e-2 off after ten steps
+ * arithmetic: a matrix of low rank is about 1e-2 to 7e-2 off after ten steps
  * and noise after twelve.  Coefficients with smaller factors (2, -1.5, 0.5)
  * leave 1e-3.
  * A matrix that holds Inf or NaN becomes NaN; one of zeros stays zero.

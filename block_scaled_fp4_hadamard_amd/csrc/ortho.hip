@@ -180,10 +180,6 @@ __device__ __forceinline__ void load_gradient(const OrthoItem& t, int64_t at, in
   for (int e = 0; e < N; ++e) o[e] *= scale;
 }
 
-__device__ __forceinline__ void load_gradient(const OrthoItem& t, int64_t at, float scale, float& o) {
-  o = (t.g_bf16 ? bf16_value(((const uint16_t*)t.g)[at]) : ((const float*)t.g)[at]) * scale;
-}
-
 // U's scale 2^12 / (|U| + eps), whose float32 might overflow or sink, in two factors; 0 for a matrix of zeros, where
 // that of the smallest eps would be Inf
 struct Scale {

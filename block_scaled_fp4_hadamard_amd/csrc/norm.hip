@@ -16,10 +16,18 @@
 // A row belongs to G lanes (16, 64: part of a wave or a wave, no LDS; 256,
 // 1024: a workgroup or a part of one), N vectors of 16 bytes a lane, so that it
 // stays in registers between its sums and its output.  From HBM, launch
-// included: forward 8192 x 4096 bf16 27 us (5.0 TB/s), 262144 x 128 21 (6.4), 2001 x
-// 5003 float32 22 (3.6: short of waves); backward 8192 x 4096 46 us, of which the
-// sums' second launch is 5, 4001 x 14335 float32 160 (4.3).  A wave for a row of
-// 4096 took 59 us forward: too few loads in flight.
+// included: forward 8192 x 4096 bf16 25 to 27 us (5.0 to 5.3 TB/s), its RMS form 23
+// (5.8), 262144 x 128 21 (6.4), 2001 x 5003 float32 22 (3.6: short of waves);
+// backward 8192 x 4096 46 us (4.4), of which the sums' second launch is 5, 4001 x
+// 14335 float32 160 (4.3).  A wave for a row of 4096 took 59 us forward: too few
+// loads in flight.
+//
+// 1024 lanes leave 128 registers each, and some kernels of two or four vectors a
+// lane do not fit them: the RMS backward of 2049 to 4096 bf16 columns spills 67
+// (8192 x 4096: 81 us, 2.5 TB/s), of 129 to 256 and 513 to 1024 columns 115 and 70;
+// the forward of 16385 to 32768 bf16 columns 94 (2048 x 20001: 84 us, 2.0 TB/s).
+// Rows wider than registers are read again for every sum: 1024 x 33001 bf16 42 us
+// forward (3.2 TB/s), 2048 x 20001 backward 126 (1.9).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include "norm_kernels.h"
@@ -569,7 +577,8 @@ __global__ void __launch_bounds__(256) norm_grad_wide_cols(const NormGradParams 
 }
 
 // dweight and dbias from the workgroups' sums: 64 columns a workgroup at a time, its 16 waves a run of the sums each.
-constexpr int64_t kSumGrid = int64_t(1) << 21;    // workgroups of 1024 lanes: a launch holds less than 2^32 lanes
+// workgroups of 1024 lanes: a launch holds less than 2^32 lanes (one of more wraps around, without an error)
+constexpr int64_t kSumGrid = int64_t(1) << 21;
 
 __global__ void __launch_bounds__(1024) norm_grad_sum(const float* parts, int count, int64_t cols, float* dweight,
                                                       float* dbias) {
@@ -620,8 +629,8 @@ Shape forward_shape(int64_t cols, int e) {
   return {0, 0, 1024};
 }
 
-// Backward.  Few rows take small workgroups, so that more CUs share them (33 x 4096: 5.4 us for 9.0); many take large
-// ones, of which each leaves its sums once.
+// Backward.  Few rows take small workgroups, so that more CUs share them (33 x 4096 RMS: the kernel 9 us for 19.6); many
+// take large ones, of which each leaves its sums once.
 Shape grad_shape(int64_t cols, int64_t rows, int e) {
   const int64_t v = (cols + e - 1) / e;
   Shape s = {0, 0, 1024};

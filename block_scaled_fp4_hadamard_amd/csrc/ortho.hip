@@ -26,12 +26,15 @@
 //
 // A list's matrices go through each product together, up to 32 in one launch:
 // the sums of squares, X, then three products a step; small ones through a single
-// kernel.  Bound by the matrix cores' power: 1024 SIMDs on random float16 data
-// and nothing else reach 1720 TFLOP/s, a large library product 1525 (8192 cubed)
-// to 1230 (4096 x 28672 x 4096 with the second operand as here).  The products of
-// a Llama-3.1-8B block's linears (symmetric ones counted half) run at 1050 to 1150;
-// the whole step of its 218 million weights takes 13.2 ms, of which the gradients'
-// and moments' passes are 1.1 (4.7 to 5 TB/s); 4096 x 4096 alone 1.35 to 1.55 by card.
+// kernel.  Bound by the matrix cores, whose power sets the clock, and by waits:
+// 1024 SIMDs on random float16 data and nothing else reach 1720 TFLOP/s (1.64 GHz), a
+// large library product 1525 (8192 cubed) to 1230 (4096 x 28672 x 4096 with the
+// second operand as here).  The products of a Llama-3.1-8B block's linears
+// (symmetric ones counted half) run at 1050 to 1150: the matrix cores are busy 53
+// to 74% of the time, at 1.6 to 1.8 GHz.  The whole step of its 218 million weights
+// takes 12.8 to 13.9 ms by card, of which the gradients' and moments' passes are 1.1
+// (4.7 to 5 TB/s); 4096 x 4096 alone 1.35 to 1.55, busy 50 to 62% at 1.8 to 2.1 GHz: one
+// round of the chip, whose first copies and epilogues nothing hides.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <utility>
@@ -344,9 +347,8 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 // places, so that the result leaves as the rows of O's transpose.
 //
 // A Llama-3.1-8B block's four kStep products, 1.79 TFLOP with all that they read
-// and write of X: 1672 us, 1070 TFLOP/s; at 1796 us the matrix cores were 56%
-// busy and the clock at 1.7 GHz: power, and a fifth for the epilogue's 8 bytes an
-// element.  Steps on the way: copies issued together 1972 us; fragments read two
+// and write of X: 1645 to 1672 us, 1070 to 1090 TFLOP/s, the matrix cores 59% busy
+// at 1.74 GHz; the epilogue's 8 bytes an element are a fifth.  Steps on the way: copies issued together 1972 us; fragments read two
 // parts ahead 1850; the copies spread over three parts 1795; the epilogue's reads
 // two rows ahead, without bounds 1708; its low part unscaled 1672.
 enum Mode { kGram, kPoly, kMix, kStep, kLast };

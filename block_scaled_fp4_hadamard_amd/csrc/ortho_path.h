@@ -140,8 +140,10 @@ inline int64_t ortho_small_bytes(const OrthoSize& z) {
 inline bool ortho_small_fits(const OrthoSize& z) { return z.m <= 128 && z.m * z.n <= 32768; }
 
 // Whether the first two steps of these matrices run as one: it replaces 3 m^2 n multiplications by 3 m^3 (symmetric
-// products counted half) and saves a pass of X, for one launch more, which large products do not notice.  A block's four
-// linears: 13.87 ms against 15.45; 4096 x 4096 alone: 1.58 either way.
+// products counted half) and saves a pass of X, for one launch more, which large products do not notice.  Joined / apart,
+// us, about the two borders: 1536 x 2048 (1.33 times as wide) 231 / 223, 2048 x 2560 (1.25) 382 / 380, 4096 x 4096 1345 /
+// 1325, 4096 x 5120 1702 / 1765, 2048 x 4096 457 / 471; 1024 x 2048 (2.1e9) 152 / 152, 1024 x 4096 (4.3e9) 201 / 209, 512 x
+// 8192 (2.1e9, left apart) 209 / 232; 4096 x 14336 3385 / 3848.
 template <typename T>
 inline bool ortho_joins(const T* list, int count) {
   double wide = 0.0, square = 0.0;

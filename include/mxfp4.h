@@ -523,7 +523,8 @@ typedef enum { MX_NORM_LAYER = 0, MX_NORM_RMS = 1 } mx_norm_kind;
  *   mean, rstd device float32 [rows], what mx_layer_norm_grad takes, or NULL;
  *              mean is NULL for MX_NORM_RMS
  * A row that holds NaN becomes NaN; one that holds Inf becomes NaN (MX_NORM_LAYER), or has rstd 0, zeros where x is
- * finite and NaN where it is not (MX_NORM_RMS).
+ * finite and NaN where it is not (MX_NORM_RMS).  Sums and squares are float32 too: a row whose squares pass its range
+ * (|d| from about 1e19 on) has rstd 0, and squares below 2^-149 are nothing beside eps.
  */
 mx_status mx_layer_norm(const void *x, mx_out type, int64_t rows, int64_t cols, int64_t ld_x, const void *weight,
                         const void *bias, mx_out weight_type, double eps, mx_norm_kind kind, void *y, int64_t ld_y,

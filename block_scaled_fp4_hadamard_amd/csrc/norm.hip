@@ -576,10 +576,10 @@ __global__ void __launch_bounds__(256) norm_grad_wide_cols(const NormGradParams 
   }
 }
 
-// dweight and dbias from the workgroups' sums: 64 columns a workgroup at a time, its 16 waves a run of the sums each.
-// workgroups of 1024 lanes: a launch holds less than 2^32 lanes (one of more wraps around, without an error)
+// Workgroups of norm_grad_sum at most: a launch holds less than 2^32 lanes (one of more wraps around, without an error).
 constexpr int64_t kSumGrid = int64_t(1) << 21;
 
+// dweight and dbias from the workgroups' sums: 64 columns a workgroup at a time, its 16 waves a run of the sums each.
 __global__ void __launch_bounds__(1024) norm_grad_sum(const float* parts, int count, int64_t cols, float* dweight,
                                                       float* dbias) {
   __shared__ float red[16][64];

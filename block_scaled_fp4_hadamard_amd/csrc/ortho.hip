@@ -348,9 +348,10 @@ __global__ void __launch_bounds__(256) ortho_start(const Args a, const OrthoStep
 //
 // A Llama-3.1-8B block's four kStep products, 1.79 TFLOP with all that they read
 // and write of X: 1645 to 1672 us, 1070 to 1090 TFLOP/s, the matrix cores 59% busy
-// at 1.74 GHz; the epilogue's 8 bytes an element are a fifth.  Steps on the way: copies issued together 1972 us; fragments read two
-// parts ahead 1850; the copies spread over three parts 1795; the epilogue's reads
-// two rows ahead, without bounds 1708; its low part unscaled 1672.
+// at 1.74 GHz; the epilogue's 8 bytes an element are a fifth.  Steps on the way:
+// copies issued together 1972 us; fragments read two parts ahead 1850; the copies
+// spread over three parts 1795; the epilogue's reads two rows ahead, without
+// bounds 1708; its low part unscaled 1672.
 enum Mode { kGram, kPoly, kMix, kStep, kLast };
 
 // 16-byte piece's place in a 128-byte LDS row: a 16-byte LDS read serves the wave in groups of 16 lanes (0-3, 12-15 and
